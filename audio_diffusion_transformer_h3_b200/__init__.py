@@ -50,6 +50,20 @@ class h3_segment_layout(ctypes.Structure):
         "video_t", "video_h", "video_w", "audio_tail")]
 
 
+class h3_rope_qk_cfg(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("attn_factor", ctypes.c_double)]
+
+
+H3_BF16, H3_FP16, H3_FP32 = 0, 1, 2
+H3_ROPE_INTERLEAVED, H3_ROPE_HALF = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "yarn": 4}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+H3_ACT_GATED = 256
+
 _c = ctypes
 _P = _c.c_void_p
 _lib.h3_segment_tokens.argtypes = [_c.POINTER(h3_segment_layout)]
@@ -88,6 +102,23 @@ _lib.h3_qkv_rope_attn_fwd.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _c.c_int32
                                       _P, h3_rope_cfg, _c.c_int64, _c.c_int32, _c.c_int32,
                                       _c.c_int32, _c.c_float, _P, _c.c_size_t, _P]
 _lib.h3_qkv_rope_attn_fwd.restype = _c.c_int
+_i32, _i64, _size = _c.c_int32, _c.c_int64, _c.c_size_t
+_lib.h3_rope_qk_freqs.argtypes = [_c.POINTER(h3_rope_qk_cfg), _P]
+_lib.h3_rope_qk_freqs.restype = _c.c_int
+_lib.h3_rope_qk_apply.argtypes = [_P, _i64, _P, _i64, _P, _i64, _P, _i64, _P,
+                                  _c.POINTER(h3_rope_qk_cfg), _i64, _i32, _i32, _i32, _i32, _P]
+_lib.h3_rope_qk_apply.restype = _c.c_int
+_lib.h3_linear_workspace_size.argtypes = [_i64, _i32, _i32, _i32]
+_lib.h3_linear_workspace_size.restype = _size
+_lib.h3_linear_fwd.argtypes = [_P, _i64, _P, _i64, _P, _P, _i64, _P, _i64, _i64, _i32, _i32,
+                               _i32, _i32, _P, _size, _P]
+_lib.h3_linear_fwd.restype = _c.c_int
+_lib.h3_cross_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32, _i32]
+_lib.h3_cross_workspace_size.restype = _size
+_lib.h3_cross_attn_fwd.argtypes = [_P, _i64, _P, _i64, _P, _i64, _P, _i64, _P, _P, _P, _i32,
+                                   _i32, _i32, _P, _i64, _i64, _i32, _i32, _i32, _c.c_float,
+                                   _i32, _P, _size, _P]
+_lib.h3_cross_attn_fwd.restype = _c.c_int
 _lib.h3_read_skip_count.argtypes = [_P, _P, _c.POINTER(_c.c_uint64)]
 _lib.h3_read_skip_count.restype = _c.c_int
 _lib.h3_selftest_bounded_wait.argtypes = [_P, _c.c_size_t, _c.c_int64, _P]
@@ -103,6 +134,8 @@ EXPORTED = ("h3_segment_tokens", "h3_build_positions", "h3_build_positions_at", 
             "h3_varlen_attn_fwd", "h3_varlen_attn_fwd_skip", "h3_read_skip_count",
             "h3_qkv_rope_gemm", "h3_qkv_rope_attn_fwd", "h3_sage_workspace_size",
             "h3_varlen_attn_fwd_sage",
+            "h3_rope_qk_freqs", "h3_rope_qk_apply", "h3_linear_workspace_size", "h3_linear_fwd",
+            "h3_cross_workspace_size", "h3_cross_attn_fwd",
             "h3_varlen_attn_fwd_static", "h3_selftest_bounded_wait",
             "h3_read_device_status", "h3_status_string", "h3_last_cuda_error")
 
@@ -214,6 +247,47 @@ def h3_varlen_attn_fwd_static(q: int, k: int, v: int, o: int, lse: int, cu_seqle
     (N*H*D <= 2^25; calls on one device must not overlap on the GPU)."""
     return int(_lib.h3_varlen_attn_fwd_static(q, k, v, o, lse, cu_seqlens, nseg, max_seqlen,
                                               pos, rope, N, H, D, softmax_scale, stream))
+
+
+def h3_rope_qk_freqs(cfg: h3_rope_qk_cfg):
+    """Angle per position of each pair, NumPy float64 [rot_dim/2] (host only)."""
+    import numpy as np
+    f = np.zeros(max(1, min(256, cfg.rot_dim // 2)), dtype=np.float64)
+    _check(_lib.h3_rope_qk_freqs(ctypes.byref(cfg), f.ctypes.data), "h3_rope_qk_freqs")
+    return f
+
+
+def h3_rope_qk_apply(q: int, ldq: int, q_out: int, ldq_out: int, k: int, ldk: int, k_out: int,
+                     ldk_out: int, positions: int, cfg: h3_rope_qk_cfg, N: int, Hq: int, Hk: int,
+                     D: int, dtype: int, stream: int) -> int:
+    return _lib.h3_rope_qk_apply(q, ldq, q_out, ldq_out, k, ldk, k_out, ldk_out, positions,
+                                 ctypes.byref(cfg), N, Hq, Hk, D, dtype, stream)
+
+
+def h3_linear_workspace_size(M: int, N: int, K: int, act: int) -> int:
+    return _lib.h3_linear_workspace_size(M, N, K, act)
+
+
+def h3_linear_fwd(x: int, ldx: int, w: int, ldw: int, bias: int, residual: int, ldr: int, y: int,
+                  ldy: int, M: int, N: int, K: int, act: int, dtype: int, workspace: int,
+                  workspace_bytes: int, stream: int) -> int:
+    return _lib.h3_linear_fwd(x, ldx, w, ldw, bias, residual, ldr, y, ldy, M, N, K, act, dtype,
+                              workspace, workspace_bytes, stream)
+
+
+def h3_cross_workspace_size(Nq: int, Hq: int, Hk: int, D: int, nseg: int, max_q: int,
+                            max_k: int) -> int:
+    return _lib.h3_cross_workspace_size(Nq, Hq, Hk, D, nseg, max_q, max_k)
+
+
+def h3_cross_attn_fwd(q: int, ldq: int, k: int, ldk: int, v: int, ldv: int, o: int, ldo: int,
+                      lse: int, cu_q: int, cu_k: int, nseg: int, max_q: int, max_k: int,
+                      key_mask: int, Nq: int, Nk: int, Hq: int, Hk: int, D: int,
+                      softmax_scale: float, dtype: int, workspace: int, workspace_bytes: int,
+                      stream: int) -> int:
+    return _lib.h3_cross_attn_fwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, cu_q, cu_k, nseg, max_q,
+                                  max_k, key_mask, Nq, Nk, Hq, Hk, D, softmax_scale, dtype,
+                                  workspace, workspace_bytes, stream)
 
 
 def h3_selftest_bounded_wait(workspace: int, workspace_bytes: int, limit_cycles: int,
@@ -480,3 +554,252 @@ def skip_count_t(workspace, stream=None) -> int:
 def device_status_t(workspace, stream=None) -> int:
     """Device status word of the last call that used ``workspace`` (syncs)."""
     return h3_read_device_status(workspace.data_ptr(), _stream(stream))
+
+
+# -------------------------------------------- layers around the attention (torch)
+
+_DTYPE_CODES: dict = {}
+
+
+def _dtype_code(dtype, fp32: bool = False) -> int:
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: H3_BF16, torch.float16: H3_FP16,
+                             torch.float32: H3_FP32})
+    code = _DTYPE_CODES.get(dtype, -1)
+    if code < 0 or (code == H3_FP32 and not fp32):
+        raise ValueError(f"dtype {dtype} is not supported")
+    return code
+
+
+def _same(first, **tensors):
+    """Every given tensor is on ``first``'s device; none asks for a gradient
+    (these calls are forward only, so a gradient would be lost in silence)."""
+    import torch
+    if not first.is_cuda:
+        raise ValueError("CUDA tensors are needed")
+    grad = torch.is_grad_enabled()
+    if grad and first.requires_grad:
+        raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+        if grad and t.requires_grad:
+            raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
+
+
+def _on(device, stream):
+    """Context in which a call on ``stream`` (None: the device's current one)
+    allocates and launches: that device is current, and what the call allocates
+    belongs to that stream. None if it is so already."""
+    import torch
+    here = torch.cuda.current_device() == device.index
+    if stream is None:
+        return None if here else torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, not on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _heads(x, name):
+    """(token stride) of a [N, H, D] tensor whose heads are contiguous."""
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [N, H, D]")
+    N, H, D = x.shape
+    s = x.stride()
+    if N > 0 and ((s[2] != 1 and D > 1) or (s[1] != D and H > 1)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return H * D if N <= 1 else s[0]
+
+
+def _rows(x, name):
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    if x.shape[0] > 0 and x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    # of a single row the stride says nothing
+    return x.stride(0) if x.shape[0] > 1 else (x.shape[1] + 7) // 8 * 8
+
+
+def _int32(x, name, shape=None):
+    import torch
+    if x.dtype != torch.int32 or not x.is_contiguous() or (shape is not None and x.shape != shape):
+        raise ValueError(f"{name} must be contiguous int32" + (f" {list(shape)}" if shape else ""))
+
+
+def rope_qk_cfg(rot_dim: int, theta: float = 10000.0, layout: str = "interleaved",
+                scaling: Optional[dict] = None) -> h3_rope_qk_cfg:
+    """``scaling``: None or a dict with ``kind`` ("linear", "ntk", "turns",
+    "yarn") and the fields of h3_rope_qk_cfg it reads (``factor``,
+    ``original_len``, ``beta_fast``, ``beta_slow``, ``attn_factor``)."""
+    s = dict(scaling or {})
+    kind = s.pop("kind", "none")
+    if kind not in ROPE_SCALINGS or layout not in ("interleaved", "half"):
+        raise ValueError(f"unknown scaling {kind!r} or layout {layout!r}")
+    values = {"factor": 1.0, "original_len": 0.0, "beta_fast": 0.0, "beta_slow": 0.0,
+              "attn_factor": 1.0}
+    for key, value in s.items():
+        if key not in values:
+            raise ValueError(f"unknown scaling field {key!r}")
+        values[key] = float(value)
+    return h3_rope_qk_cfg(int(rot_dim), H3_ROPE_HALF if layout == "half" else H3_ROPE_INTERLEAVED,
+                          ROPE_SCALINGS[kind], 0, float(theta), values["factor"],
+                          values["original_len"], values["beta_fast"], values["beta_slow"],
+                          values["attn_factor"])
+
+
+def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 10000.0,
+              layout: str = "interleaved", scaling: Optional[dict] = None, out=None, stream=None):
+    """(q, k) rotated by whole-number positions through h3_rope_qk_apply. q
+    [N, Hq, D], k [N, Hk, D] or None, bf16, fp16 or fp32, heads contiguous (a
+    token stride is free); positions int32 [N]. ``out``: (q_out, k_out), which
+    may be (q, k). The gradient of q and k is this call on the outputs'
+    gradients with negated positions."""
+    import torch
+    _same(q, k=k, positions=positions)
+    ctx = _on(q.device, stream)
+    if ctx is not None:
+        with ctx:
+            return rope_qk_t(q, k, positions, rot_dim, theta, layout, scaling, out)
+    code = _dtype_code(q.dtype, fp32=True)
+    N, Hq, D = q.shape
+    ldq = _heads(q, "q")
+    _int32(positions, "positions", (N,))
+    cfg = rope_qk_cfg(D if rot_dim is None else rot_dim, theta, layout, scaling)
+    Hk, ldk, kp = 0, 0, 0
+    if k is not None:
+        if k.dtype != q.dtype or k.dim() != 3 or k.shape[0] != N or k.shape[2] != D:
+            raise ValueError("k must be [N, Hk, D] of q's type")
+        Hk, ldk, kp = k.shape[1], _heads(k, "k"), k.data_ptr()
+    if out is None:
+        qo = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty((N, Hk, D), dtype=q.dtype, device=q.device)
+        ldqo, ldko = Hq * D, Hk * D
+    else:
+        qo, ko = out
+        _same(q, q_out=qo, k_out=ko)
+        if qo.shape != q.shape or qo.dtype != q.dtype or (k is None) != (ko is None) or (
+                k is not None and (ko.shape != k.shape or ko.dtype != q.dtype)):
+            raise ValueError("out must have the shapes and type of (q, k)")
+        ldqo, ldko = _heads(qo, "q_out"), 0 if ko is None else _heads(ko, "k_out")
+    _check(h3_rope_qk_apply(q.data_ptr(), ldq, qo.data_ptr(), ldqo, kp, ldk,
+                            0 if ko is None else ko.data_ptr(), ldko, positions.data_ptr(), cfg,
+                            N, Hq, Hk, D, code, torch.cuda.current_stream().cuda_stream),
+           "h3_rope_qk_apply")
+    return qo, ko
+
+
+def linear_workspace_for(M: int, N: int, K: int, gated: bool = False, device=None):
+    """Workspace of linear_t for x [M, K] and N output features."""
+    import torch
+    n = h3_linear_workspace_size(M, N, K, H3_ACT_GATED if gated else 0)
+    if n == 0:
+        raise ValueError("sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=None, out=None,
+             workspace=None, stream=None):
+    """act(x w^T + bias) + residual through h3_linear_fwd. x [M, K], w [N, K],
+    bf16 or fp16, rows 16-byte aligned (row strides a multiple of 8). ``gated``:
+    w [2N, K], act(first half) * (second half). ``out`` may be ``residual``."""
+    import torch
+    _same(x, w=w, bias=bias, residual=residual, out=out, workspace=workspace)
+    ctx = _on(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return linear_t(x, w, bias, act, gated, residual, out, workspace)
+    code = _dtype_code(x.dtype)
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}")
+    ldx, ldw = _rows(x, "x"), _rows(w, "w")
+    M, K = x.shape
+    N = w.shape[0]
+    if w.dtype != x.dtype or w.shape[1] != K or (gated and N % 2):
+        raise ValueError(f"w must be [{'2N' if gated else 'N'}, {K}] of x's type")
+    if bias is not None and (bias.dtype != x.dtype or bias.shape != (N,) or
+                             not bias.is_contiguous()):
+        raise ValueError(f"bias must be contiguous [{N}] of x's type")
+    a = ACTIVATIONS[act]
+    if gated:
+        N //= 2
+        a += H3_ACT_GATED
+    ldr = 0
+    if residual is not None:
+        if residual.shape != (M, N) or residual.dtype != x.dtype:
+            raise ValueError(f"residual must be [{M}, {N}] of x's type")
+        ldr = _rows(residual, "residual")
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    elif out.shape != (M, N) or out.dtype != x.dtype:
+        raise ValueError(f"out must be [{M}, {N}] of x's type")
+    if workspace is None:
+        workspace = linear_workspace_for(M, N, K, gated, x.device)
+    _check(h3_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw,
+                         0 if bias is None else bias.data_ptr(),
+                         0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
+                         _rows(out, "out"), M, N, K, a, code, workspace.data_ptr(),
+                         workspace.numel(), torch.cuda.current_stream().cuda_stream),
+           "h3_linear_fwd")
+    return out
+
+
+def cross_workspace_for(Nq: int, Hq: int, Hk: int, D: int, nseg: int, max_q: int, max_k: int,
+                        device=None):
+    """Workspace of cross_attn_fwd_t for these sizes."""
+    import torch
+    n = h3_cross_workspace_size(Nq, Hq, Hk, D, nseg, max_q, max_k)
+    if n == 0:
+        raise ValueError("sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
+                     softmax_scale: Optional[float] = None, out=None, return_lse: bool = False,
+                     workspace=None, stream=None):
+    """O (and LSE [Hq, Nq] if asked) through h3_cross_attn_fwd: the queries of
+    each segment attend to its keys in another packed sequence. q [Nq, Hq, D],
+    k, v [Nk, Hk, D], bf16 or fp16, heads contiguous, token strides a multiple
+    of 8; cu_q, cu_k int32 [nseg + 1]; key_mask bool or uint8 [Nk], False: no
+    query attends to this key. A row without keys gets 0 (LSE -inf). Rows
+    behind cu_q[-1] are not written."""
+    import torch
+    _same(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, key_mask=key_mask, out=out, workspace=workspace)
+    ctx = _on(q.device, stream)
+    if ctx is not None:
+        with ctx:
+            return cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q, max_k, key_mask, softmax_scale,
+                                    out, return_lse, workspace)
+    code = _dtype_code(q.dtype)
+    ldq, ldk, ldv = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    Nq, Hq, D = q.shape
+    Nk, Hk, _ = k.shape
+    if k.dtype != q.dtype or v.dtype != q.dtype or k.shape != v.shape or k.shape[2] != D:
+        raise ValueError("k and v must be [Nk, Hk, D] of q's type")
+    nseg = cu_q.numel() - 1
+    _int32(cu_q, "cu_q", (nseg + 1,))
+    _int32(cu_k, "cu_k", (nseg + 1,))
+    if key_mask is not None and (key_mask.shape != (Nk,) or not key_mask.is_contiguous() or
+                                 key_mask.dtype not in (torch.bool, torch.uint8)):
+        raise ValueError(f"key_mask must be contiguous bool or uint8 [{Nk}]")
+    if out is None:
+        out = torch.empty((Nq, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    lse = torch.empty((Hq, Nq), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        workspace = cross_workspace_for(Nq, Hq, Hk, D, nseg, int(max_q), int(max_k), q.device)
+    scale = (1.0 / math.sqrt(D)) if softmax_scale is None else float(softmax_scale)
+    _check(h3_cross_attn_fwd(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                             out.data_ptr(), _heads(out, "out"),
+                             0 if lse is None else lse.data_ptr(), cu_q.data_ptr(),
+                             cu_k.data_ptr(), nseg, int(max_q), int(max_k),
+                             0 if key_mask is None else key_mask.data_ptr(), Nq, Nk, Hq, Hk, D,
+                             scale, code, workspace.data_ptr(), workspace.numel(),
+                             torch.cuda.current_stream().cuda_stream),
+           "h3_cross_attn_fwd")
+    return (out, lse) if return_lse else out

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "h3attn.h"
+#include "host_util.h"
 #include "attn_fwd.cuh"
 #include "attn_sage.cuh"
 #include "qkv_gemm.cuh"
@@ -22,42 +23,15 @@
 
 namespace {
 
-thread_local int32_t g_last_cuda_error = 0;
-
-h3_status cuda_fail(cudaError_t e) {
-    g_last_cuda_error = static_cast<int32_t>(e);
-    return H3_ERR_CUDA;
-}
-
-constexpr size_t kStatusBytes = 256;
+using h3host::aligned;
+using h3host::cuda_fail;
+using h3host::encode_tiled;
+using h3host::EncodeTiledFn;
+using h3host::kStatusBytes;
+using h3host::round_up;
 
 // Row tiles of the QKV GEMM that sweep the column tiles together (L2 reuse).
 constexpr int32_t kQkvGroupM = 32;
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// ---------------------------------------------------------------- driver API
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(ptr);
-    }();
-    return fn;
-}
 
 // Per-device one-time set-up: capability check, SM count, kernel attributes.
 struct DeviceInfo {
@@ -692,6 +666,6 @@ const char *h3_status_string(h3_status s) {
     return "unknown status";
 }
 
-int32_t h3_last_cuda_error(void) { return g_last_cuda_error; }
+int32_t h3_last_cuda_error(void) { return h3host::g_last_cuda_error; }
 
 }  // extern "C"

@@ -279,6 +279,160 @@ h3_status h3_qkv_rope_attn_fwd(const void *x, const void *w, void *q, void *k, v
                                int64_t N, int32_t K, int32_t H, int32_t D, float softmax_scale,
                                void *workspace, size_t workspace_bytes, h3_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The layers around the attention: 1-D rotary positions, cross attention to
+ * an encoder's states, and the linear layers. Unlike the calls above they
+ * take bf16 or fp16 (the rotary call fp32 too) and strided rows. `dtype`
+ * names the element type of every tensor of a call that is not otherwise
+ * typed; a row (token) stride `ld*` counts elements. All are forward only.
+ * ------------------------------------------------------------------------ */
+typedef enum h3_dtype { H3_BF16 = 0, H3_FP16 = 1, H3_FP32 = 2 } h3_dtype;
+
+/* Which channels of the rotated part [0, rot_dim) form pair j (j < rot_dim/2):
+ * (2j, 2j + 1), or (j, j + rot_dim/2). */
+typedef enum h3_rope_layout { H3_ROPE_INTERLEAVED = 0, H3_ROPE_HALF = 1 } h3_rope_layout;
+
+/* How the angle per position f_j = theta^(-2j/rot_dim) of pair j is changed
+ * for contexts longer than original_len, s = factor:
+ *   NONE    f_j
+ *   LINEAR  f_j / s                       (positions interpolated)
+ *   NTK     f_j with theta s^(r/(r-2)), r = rot_dim > 2    (base changed)
+ *   TURNS   g f_j + (1 - g) f_j / s, g = (n_j - beta_slow) / (beta_fast -
+ *           beta_slow) clamped to [0, 1], n_j = original_len f_j / (2 pi) the
+ *           turns pair j makes over the original length
+ *   YARN    the same with g = 1 - (j - lo) / (hi - lo) clamped, where lo and
+ *           hi are the pair numbers at which n_j is beta_fast and beta_slow
+ *           (real j), rounded down and up and clamped to [0, rot_dim - 1]
+ *           (hi - lo at least 0.001). */
+typedef enum h3_rope_scaling {
+    H3_ROPE_SCALE_NONE = 0,
+    H3_ROPE_SCALE_LINEAR = 1,
+    H3_ROPE_SCALE_NTK = 2,
+    H3_ROPE_SCALE_TURNS = 3,
+    H3_ROPE_SCALE_YARN = 4
+} h3_rope_scaling;
+
+typedef struct h3_rope_qk_cfg {
+    int32_t rot_dim; /* even, 2 <= rot_dim <= D: the channels that rotate */
+    int32_t layout;  /* h3_rope_layout */
+    int32_t scaling; /* h3_rope_scaling */
+    int32_t reserved; /* 0 */
+    double theta;    /* > 0 (> 1 with YARN) */
+    double factor;   /* > 0; read by every scaling but NONE */
+    double original_len, beta_fast, beta_slow; /* TURNS, YARN: > 0, fast > slow */
+    double attn_factor; /* cos and sin are multiplied by it; finite (1: none) */
+} h3_rope_qk_cfg;
+
+/* The angle per position of each pair, freqs[rot_dim/2], in double. Host only.
+ * H3_ERR_INVALID_ARG for a cfg that h3_rope_qk_apply would refuse. */
+h3_status h3_rope_qk_freqs(const h3_rope_qk_cfg *cfg, double *freqs);
+
+/* Rotary embedding with one whole-number position a token, for q and k of
+ * different head counts in one launch. Pair (x0, x1) of the layout becomes
+ * a (x0 cos - x1 sin), a (x0 sin + x1 cos) with angle position * f_j and
+ * a = attn_factor; channels [rot_dim, D) are copied.
+ *   q, q_out : device [N, Hq, D], token strides ldq, ldq_out >= Hq * D, heads
+ *              contiguous; q_out may equal q (with equal strides); any other
+ *              overlap is undefined. k, k_out, ldk, ldk_out likewise with Hk;
+ *              k and k_out NULL and Hk = 0: q alone.
+ *   positions: device int32 [N], any value. Angles are exact to 2^-33 turns
+ *              at every position (fixed-point phase), cos and sin fp32.
+ *   N >= 0 (0 is a no-op), 1 <= Hq <= 65535, 0 <= Hk <= 65535, 2 <= D <= 512,
+ *   N * ld < 2^47, dtype H3_BF16, H3_FP16 or H3_FP32; pointers aligned to
+ *   their element (16-byte aligned rows and halves take the vector path).
+ * Rounded once to dtype. The gradient with respect to q and k is the same
+ * call on the outputs' gradients with negated positions. Deterministic; one
+ * kernel launch. */
+h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_out,
+                           const void *k, int64_t ldk, void *k_out, int64_t ldk_out,
+                           const int32_t *positions, const h3_rope_qk_cfg *cfg, int64_t N,
+                           int32_t Hq, int32_t Hk, int32_t D, int32_t dtype,
+                           h3_stream_t stream);
+
+/* Activation of h3_linear_fwd. H3_ACT_GATED is added to one of the others. */
+typedef enum h3_act {
+    H3_ACT_NONE = 0,
+    H3_ACT_RELU = 1,
+    H3_ACT_GELU = 2,      /* x/2 (1 + erf(x / sqrt 2)) */
+    H3_ACT_GELU_TANH = 3, /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    H3_ACT_SILU = 4,      /* x / (1 + exp(-x)) */
+    H3_ACT_GATED = 256
+} h3_act;
+
+/* Bytes of device workspace h3_linear_fwd needs for these sizes (`act` tells
+ * whether the layer is gated): a 256-byte status block and, where few rows
+ * make it split the sum over K, fp32 partial products. 0 for a bad size. */
+size_t h3_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act);
+
+/* Linear layer with bias, activation and residual in the product's epilogue:
+ *     y = act(x w^T + bias) + residual
+ *     gated: y = act(x wg^T + bias_g) * (x wu^T + bias_u) + residual,
+ *            wg = w[0:N], wu = w[N:2N] and bias likewise
+ * (the DiT's output projection, feed-forward and modulation linears: "Day 0
+ * Support for MiniMax-H3 on AMD Instinct GPUs", section "The diffusion
+ * transformer (DiT)"; "MiniMax H3" vLLM-Omni recipe, section "Online FP8
+ * quantization" names gate_up as one product).
+ *   x        : device [M, K], row stride ldx; w: device [N, K] ([2N, K] gated),
+ *              row stride ldw; both 16-byte aligned, ldx, ldw >= K multiples of 8.
+ *   bias     : device [N] ([2N] gated) or NULL; residual: device [M, N], row
+ *              stride ldr >= N, or NULL; y: device [M, N], row stride ldy >= N.
+ *              Element-aligned. y may equal residual (with equal strides); any
+ *              other overlap with an input is undefined.
+ *   act      : h3_act, for a gated layer plus H3_ACT_GATED.
+ *   M >= 0 (0 is a no-op), M < 2^31 - 256; 1 <= N, K <= 2^20, any values;
+ *   dtype H3_BF16 or H3_FP16.
+ *   workspace: device, 256-byte aligned, >= h3_linear_workspace_size bytes;
+ *              not shared by calls that run concurrently.
+ * fp32 accumulation, bias, activation and residual in fp32, one rounding.
+ * Deterministic (also where the sum over K is split: the parts are added in
+ * their order). */
+h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
+                        const void *bias, const void *residual, int64_t ldr, void *y,
+                        int64_t ldy, int64_t M, int32_t N, int32_t K, int32_t act,
+                        int32_t dtype, void *workspace, size_t workspace_bytes,
+                        h3_stream_t stream);
+
+/* Bytes of device workspace h3_cross_attn_fwd needs: a 256-byte status block
+ * and, where few query rows make it split the keys, fp32 partial results.
+ * 0 for a bad size. */
+size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, int32_t nseg,
+                               int32_t max_q, int32_t max_k);
+
+/* Packed varlen cross attention: the queries of segment s attend to the keys
+ * of segment s of another packed sequence (an encoder's states, such as the
+ * text's). For query head h, key head h / (Hq / Hk):
+ *     O = softmax(softmax_scale * q k^T) v over the segment's keys that the
+ *     mask keeps, LSE = natural log of the row's sum of exponentials.
+ * A row without keys (an empty key segment, or none kept) gets O = 0 and
+ * LSE = -infinity.
+ *   q, o     : device [Nq, Hq, D], token strides ldq, ldo >= Hq * D;
+ *   k, v     : device [Nk, Hk, D], token strides ldk, ldv >= Hk * D; all
+ *              16-byte aligned with strides a multiple of 8, heads contiguous;
+ *              o must not overlap an input. k, v may be NULL if Nk = 0.
+ *   lse      : device fp32 [Hq, Nq] or NULL.
+ *   cu_q, cu_k : device int32 [nseg + 1], non-decreasing from 0, last value at
+ *              most Nq (Nk); tokens behind it are not read (k, v may hold
+ *              anything there) and their rows of o and lse not written. No
+ *              length may exceed max_q (max_k). A violation leaves o and lse
+ *              as they were and sets H3_ERR_BAD_SEQLENS in the status word.
+ *   max_q, max_k : 1 <= max_q <= Nq, 0 <= max_k <= Nk.
+ *   key_mask : device uint8 [Nk], 0 = no query attends to this key; or NULL.
+ *              What k and v hold at such keys has no influence, whatever it is.
+ *   Nq, Nk   : 0 <= Nq, Nk < 2^31 (Nq = 0 is a no-op); 1 <= Hk <= Hq <= 65535,
+ *              Hq a multiple of Hk; D in {64, 128}; 1 <= nseg <= 65535;
+ *              softmax_scale finite, >= 0; dtype H3_BF16 or H3_FP16.
+ *   workspace: device, 256-byte aligned, >= h3_cross_workspace_size bytes; not
+ *              shared by calls that run concurrently.
+ * fp32 scores, sums and accumulation; P is rounded to dtype before the PV
+ * product. Deterministic, the split over keys included. */
+h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk,
+                            const void *v, int64_t ldv, void *o, int64_t ldo, float *lse,
+                            const int32_t *cu_q, const int32_t *cu_k, int32_t nseg,
+                            int32_t max_q, int32_t max_k, const uint8_t *key_mask, int64_t Nq,
+                            int64_t Nk, int32_t Hq, int32_t Hk, int32_t D,
+                            float softmax_scale, int32_t dtype, void *workspace,
+                            size_t workspace_bytes, h3_stream_t stream);
+
 /* Bytes of the scratch array compiled into the library for
  * h3_varlen_attn_fwd_static: a 256-byte status block plus room for the
  * rotated keys of N*H*D <= 2^25 elements (64 MiB of bf16). */
