@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libh3attn.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("h3attn.cu", "h3attn_static.cu", "h3layers.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "sm100.cuh", "rope.cuh", "attn_fwd.cuh", "attn_sage.cuh", "qkv_gemm.cuh", "host_util.h",
-    "rope_qk.cuh", "linear.cuh", "cross_attn.cuh")] + [
+    "layer_types.cuh", "rope_qk.cuh", "linear.cuh", "cross_attn.cuh")] + [
     os.path.join(INCLUDE, "h3attn.h")]
 
 

@@ -125,23 +125,91 @@ bool linear_sizes_ok(int64_t M, int32_t N, int32_t K, int32_t act) {
            K <= (1 << 20) && a >= H3_ACT_NONE && a <= H3_ACT_SILU;
 }
 
-template <typename T, int Act>
-void launch_linear_act(const h3::LinearParams &p, bool gated, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((p.N + 63) / 64), static_cast<unsigned>((p.M + 63) / 64));
-    if (gated) h3::linear_kernel<T, Act, true><<<grid, 256, 0, st>>>(p);
-    else h3::linear_kernel<T, Act, false><<<grid, 256, 0, st>>>(p);
+// Rows of x up to which the weight rows are the MMA's rows (linear_skinny_kernel).
+constexpr int64_t kSkinnyRows = 128;
+// CTAs the skinny kernel aims at: two on each of 148 SMs.
+constexpr int kSkinnyCtas = 296;
+
+int skinny_tiles(int32_t N) { return (N + 127) / 128; }
+
+// Parts of the sum over K: as many as fill the CTAs, of 8 steps of 64 at least
+// (a shorter part is mostly the pipeline's start).
+int skinny_splits(int32_t N, int32_t K) {
+    const int n_k = (K + 63) / 64;
+    return std::max(1, std::min({kSkinnyCtas / skinny_tiles(N), n_k / 8, 32}));
 }
 
-template <typename T>
-void launch_linear(const h3::LinearParams &p, int act, cudaStream_t st) {
-    const bool gated = (act & H3_ACT_GATED) != 0;
-    switch (act & ~H3_ACT_GATED) {
-        case H3_ACT_RELU: return launch_linear_act<T, 1>(p, gated, st);
-        case H3_ACT_GELU: return launch_linear_act<T, 2>(p, gated, st);
-        case H3_ACT_GELU_TANH: return launch_linear_act<T, 3>(p, gated, st);
-        case H3_ACT_SILU: return launch_linear_act<T, 4>(p, gated, st);
-        default: return launch_linear_act<T, 0>(p, gated, st);
+int skinny_cols(int64_t M) { return static_cast<int>((M + 15) / 16 * 16); }
+
+// Bytes behind the status block: arrival counters, then the parts.
+size_t skinny_counter_bytes(int32_t N) {
+    return h3host::round_up(static_cast<size_t>(skinny_tiles(N)) * 4, 256);
+}
+
+// Columns of a tile: the widest part of the work is ceil(tiles / SMs) tiles a
+// CTA, each costing its columns plus about 24 columns' worth of start and end
+// (measured between 16 and 40).
+int tile_columns(int64_t M, int32_t products, int sms, bool gated) {
+    int best = 256;
+    int64_t best_cost = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= gated ? 64 : 32) {   // whole chunks of 32 outputs
+        const int64_t tiles = (M + 127) / 128 * ((static_cast<int64_t>(products) + bn - 1) / bn);
+        const int64_t cost = (tiles + sms - 1) / sms * (bn + 24);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = bn;
+        }
     }
+    return best;
+}
+
+// TMA map over `rows` x `cols` 16-bit elements, row stride ld, box 64 x box_rows,
+// 128-byte swizzle, zeros out of bounds.
+h3_status make_rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols,
+                        int64_t ld, uint32_t box_rows) {
+    const h3host::EncodeTiledFn enc = h3host::encode_tiled();
+    if (enc == nullptr) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims,
+                           strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? H3_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+template <typename Kernel>
+h3_status launch_mma(Kernel kernel, int grid, int threads, int smem, const CUtensorMap &a,
+                     const CUtensorMap &b, const h3::LinearParams &p, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    kernel<<<grid, threads, smem, st>>>(a, b, p);
+    return launched();
+}
+
+template <typename T, bool Gated>
+h3_status launch_linear(h3::LinearParams &p, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                        int sms, cudaStream_t st) {
+    const int64_t w_rows = Gated ? 2 * static_cast<int64_t>(p.N) : p.N;
+    CUtensorMap tx, tw;
+    h3_status s;
+    if (p.M <= kSkinnyRows) {
+        using C = h3::LinearSkinny;
+        if ((s = make_rows_map(&tx, x, p.M, p.K, ldx, p.cols)) != H3_OK ||
+            (s = make_rows_map(&tw, w, w_rows, p.K, ldw, C::BM)) != H3_OK)
+            return s;
+        return launch_mma(h3::linear_skinny_kernel<T, Gated>, p.tiles * p.splits, C::THREADS,
+                          C::SMEM_BYTES, tx, tw, p, st);
+    }
+    using C = h3::LinearTile;
+    const int out_cols = Gated ? p.bn / 2 : p.bn;
+    if ((s = make_rows_map(&tx, x, p.M, p.K, ldx, C::BM)) != H3_OK ||
+        (s = make_rows_map(&tw, w, w_rows, p.K, ldw, out_cols)) != H3_OK)
+        return s;
+    return launch_mma(h3::linear_tile_kernel<T, Gated>, std::min(p.n_tiles, sms), C::THREADS,
+                      C::SMEM_BYTES, tx, tw, p, st);
 }
 
 // ------------------------------------------------------------ cross attention
@@ -214,7 +282,11 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
 }
 
 size_t h3_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act) {
-    return linear_sizes_ok(M, N, K, act) ? kStatusBytes : 0;
+    if (!linear_sizes_ok(M, N, K, act)) return 0;
+    if (M > kSkinnyRows || skinny_splits(N, K) == 1) return kStatusBytes;
+    const size_t part = static_cast<size_t>(act & H3_ACT_GATED ? 2 : 1) * skinny_cols(M) * 128 * 4;
+    return kStatusBytes + skinny_counter_bytes(N) +
+           static_cast<size_t>(skinny_tiles(N)) * skinny_splits(N, K) * part;
 }
 
 h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
@@ -242,16 +314,47 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
     h3_status st = device_info(&d);
     if (st != H3_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), cs);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const bool gated = (act & H3_ACT_GATED) != 0, skinny = M <= kSkinnyRows;
+    const bool split = M > 0 && skinny && skinny_splits(N, K) > 1;
+    const cudaError_t e = cudaMemsetAsync(
+        ws, 0, split ? kStatusBytes + skinny_counter_bytes(N) : sizeof(int), cs);
     if (e != cudaSuccess) return cuda_fail(e);
     if (M == 0) return H3_OK;
     h3::LinearParams p;
-    p.x = x; p.w = w; p.bias = bias; p.residual = residual; p.y = y;
-    p.ldx = ldx; p.ldw = ldw; p.ldr = ldr; p.ldy = ldy;
-    p.M = M; p.N = N; p.K = K;
-    if (dtype == H3_BF16) launch_linear<__nv_bfloat16>(p, act, cs);
-    else launch_linear<__half>(p, act, cs);
-    return launched();
+    std::memset(&p, 0, sizeof(p));
+    p.bias = bias; p.residual = residual; p.y = y;
+    p.ldr = ldr; p.ldy = ldy;
+    p.status = static_cast<int *>(workspace);
+    p.M = static_cast<int32_t>(M); p.N = N; p.K = K; p.act = act & ~H3_ACT_GATED;
+    p.vec_y = aligned(y, 16) && ldy % 8 == 0;
+    p.vec_r = aligned(residual, 16) && ldr % 8 == 0;
+    if (skinny) {
+        using C = h3::LinearSkinny;
+        p.cols = skinny_cols(M);
+        p.tiles = skinny_tiles(N);
+        p.splits = skinny_splits(N, K);
+        p.stages = std::min(C::MAX_STAGES, C::RING_BYTES / ((gated ? 2 : 1) * C::W_BYTES + p.cols * C::BK * 2));
+        p.arrived = reinterpret_cast<int *>(ws + kStatusBytes);
+        p.parts = reinterpret_cast<float *>(ws + kStatusBytes + skinny_counter_bytes(N));
+    } else {
+        using C = h3::LinearTile;
+        const int64_t products = gated ? 2 * static_cast<int64_t>(N) : N;
+        p.bn = tile_columns(M, static_cast<int32_t>(products), d->sms, gated);
+        p.stages = std::min(C::MAX_STAGES, C::RING_BYTES / (C::A_BYTES + p.bn * C::BK * 2));
+        const int out_cols = gated ? p.bn / 2 : p.bn;
+        p.n_row_tiles = static_cast<int32_t>((M + C::BM - 1) / C::BM);
+        p.n_col_tiles = (N + out_cols - 1) / out_cols;
+        const int64_t tiles = static_cast<int64_t>(p.n_row_tiles) * p.n_col_tiles;
+        if (tiles > INT32_MAX - 4096) return H3_ERR_INVALID_ARG;
+        p.n_tiles = static_cast<int32_t>(tiles);
+        p.group_m = 32;
+    }
+    if (dtype == H3_BF16)
+        return gated ? launch_linear<__nv_bfloat16, true>(p, x, ldx, w, ldw, d->sms, cs)
+                     : launch_linear<__nv_bfloat16, false>(p, x, ldx, w, ldw, d->sms, cs);
+    return gated ? launch_linear<__half, true>(p, x, ldx, w, ldw, d->sms, cs)
+                 : launch_linear<__half, false>(p, x, ldx, w, ldw, d->sms, cs);
 }
 
 size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, int32_t nseg,

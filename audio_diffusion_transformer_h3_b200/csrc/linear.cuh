@@ -1,72 +1,503 @@
-// Linear layer with bias, activation and residual in its epilogue.
+// Linear layer with bias, activation and residual in the product's epilogue:
+// y = act(x w^T + bias) + residual, or act(x wg^T + bg) (x wu^T + bu) + residual.
+//
+// Two kernels, both fed by TMA through a ring of 64-wide K steps, multiplied
+// by tcgen05.mma into fp32 TMEM accumulators, every wait bounded:
+//   linear_tile_kernel  rows of x are the 128 rows of the MMA, BN weight rows
+//       its columns. Persistent, two accumulators, so that a tile's epilogue
+//       runs under the next tile's main loop. Bound by the tensor cores.
+//   linear_skinny_kernel  few rows of x: weight rows are the MMA's 128 rows
+//       and x its 16..128 columns, so nothing of the MMA is spent on absent
+//       rows. Bound by reading w once; to have all SMs read, the sum over K
+//       is split over CTAs and the last of a tile's CTAs to finish adds the
+//       fp32 parts in their order.
+// A gated layer keeps the gate and the up product of the same outputs side by
+// side in TMEM and multiplies them in the epilogue.
 #pragma once
 
 #include <cstdint>
 
-#include "rope_qk.cuh"
+#include "layer_types.cuh"
 
 namespace h3 {
 
 struct LinearParams {
-    const void *x, *w, *bias, *residual;
+    const void *bias, *residual;
     void *y;
-    int64_t ldx, ldw, ldr, ldy, M;
-    int32_t N, K;
+    int64_t ldr, ldy;
+    int *status;
+    int32_t M, N, K, act;     // act: h3_act without the gate
+    int32_t vec_y, vec_r;     // y / residual rows allow 16-byte accesses
+    // tile kernel
+    int32_t bn, stages, n_row_tiles, n_col_tiles, n_tiles, group_m;
+    // skinny kernel
+    int32_t cols, splits, tiles;
+    float *parts;             // [tile][split][product][col][128]
+    int *arrived;             // [tile], zero at launch
 };
 
-// Act: h3_act without the gate bit.
-template <int Act>
-__device__ __forceinline__ float activate(float x) {
-    if constexpr (Act == 1) return x < 0.0f ? 0.0f : x;   // keeps NaN
-    if constexpr (Act == 2) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
-    if constexpr (Act == 3) {
-        // x/2 (1 + tanh u) = x / (1 + exp(-2u))
-        const float u2 = 1.5957691216057308f * (x + 0.044715f * x * x * x);
-        return x / (1.0f + __expf(-u2));
+// act in place on V values; the switch is uniform over the grid.
+template <int V>
+__device__ __forceinline__ void activate(float (&x)[V], int act) {
+    switch (act) {
+        case 1:
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = x[i] < 0.0f ? 0.0f : x[i];   // keeps NaN
+            break;
+        case 2:
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                x[i] = 0.5f * x[i] * (1.0f + erff(x[i] * 0.70710678118654752f));
+            break;
+        case 3:
+            // x/2 (1 + tanh u) = x / (1 + exp(-2u))
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float u2 = 1.5957691216057308f * (x[i] + 0.044715f * x[i] * x[i] * x[i]);
+                x[i] = __fdividef(x[i], 1.0f + __expf(-u2));
+            }
+            break;
+        case 4:
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = __fdividef(x[i], 1.0f + __expf(-x[i]));
+            break;
+        default: break;
     }
-    if constexpr (Act == 4) return x / (1.0f + __expf(-x));
-    return x;
 }
 
-// 64 x 64 outputs a block, 4 x 4 a thread, fp32 FMAs.
-template <typename T, int Act, bool Gated>
-__global__ void __launch_bounds__(256) linear_kernel(const LinearParams p) {
-    constexpr int B = 64, KB = 16, W = Gated ? 2 : 1;
-    __shared__ float xs[KB][B + 1], ws[W][KB][B + 1];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * B;
-    const int n0 = blockIdx.x * B;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const T *x = static_cast<const T *>(p.x), *w = static_cast<const T *>(p.w);
-    float acc[W][4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += KB) {
-        for (int i = threadIdx.x; i < B * KB; i += 256) {
-            const int r = i / KB, k = i % KB;
-            const bool kin = k0 + k < p.K;
-            xs[k][r] = kin && m0 + r < p.M ? to_f32(x[(m0 + r) * p.ldx + k0 + k]) : 0.0f;
-            for (int g = 0; g < W; ++g)
-                ws[g][k][r] = kin && n0 + r < p.N
-                    ? to_f32(w[(static_cast<int64_t>(g) * p.N + n0 + r) * p.ldw + k0 + k]) : 0.0f;
+// --------------------------------------------------------------- tile kernel
+
+struct LinearTile {
+    static constexpr int BM = 128, BK = 64, MAX_BN = 256;
+    static constexpr int A_BYTES = BM * BK * 2;
+    static constexpr int MAX_STAGES = 8;
+    static constexpr int RING_BYTES = 4 * (A_BYTES + MAX_BN * BK * 2);   // 192 KB
+    static constexpr int OFF_BIAS = RING_BYTES;                          // 256 fp32
+    static constexpr int OFF_BAR = OFF_BIAS + MAX_BN * 4;
+    static constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;              // + alignment slack
+    static constexpr int THREADS = 192, TMA_WARP = 4, MMA_WARP = 5;
+};
+
+enum : int {
+    LT_FULL = 0, LT_EMPTY = 8, LT_ACC_FULL = 16, LT_ACC_EMPTY = 18, LT_DRAIN = 20, LT_COUNT = 21
+};
+
+// Tile number -> (row tile, column tile): group_m row tiles sweep the columns
+// together, so the x rows and w slices in flight stay in L2.
+__device__ __forceinline__ void linear_tile_at(const LinearParams &p, int tile, int &m, int &n) {
+    const int per_group = p.group_m * p.n_col_tiles;
+    const int group = tile / per_group, first = group * p.group_m;
+    const int left = p.n_row_tiles - first, gm = left < p.group_m ? left : p.group_m;
+    const int in_group = tile - group * per_group;
+    m = first + in_group % gm;
+    n = in_group / gm;
+}
+
+// 32 finished fp32 values of row `row`, columns [col, col + 32): residual, one
+// rounding, store.
+template <typename T>
+__device__ __forceinline__ void linear_store32(const LinearParams &p, int row, int col,
+                                               float (&v)[32]) {
+    const T *res = static_cast<const T *>(p.residual);
+    T *y = static_cast<T *>(p.y) + row * p.ldy + col;
+    const int valid = p.N - col;
+    if (res != nullptr) {
+        res += row * p.ldr + col;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+            if (p.vec_r && c + 8 <= valid) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(res + c);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<T>(ww[i]);
+                    v[c + 2 * i] += f.x;
+                    v[c + 2 * i + 1] += f.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < valid) v[c + i] += to_f32(res[c + i]);
+            }
         }
-        __syncthreads();
-        for (int k = 0; k < KB; ++k)
-            for (int g = 0; g < W; ++g)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j)
-                        acc[g][i][j] = fmaf(xs[k][ty * 4 + i], ws[g][k][tx * 4 + j], acc[g][i][j]);
-        __syncthreads();
     }
-    const T *bias = static_cast<const T *>(p.bias), *res = static_cast<const T *>(p.residual);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i;
-            const int n = n0 + tx * 4 + j;
-            if (m >= p.M || n >= p.N) continue;
-            float v = acc[0][i][j] + (bias ? to_f32(bias[n]) : 0.0f);
-            v = activate<Act>(v);
-            if (Gated) v *= acc[W - 1][i][j] + (bias ? to_f32(bias[p.N + n]) : 0.0f);
-            if (res) v += to_f32(res[m * p.ldr + n]);
-            static_cast<T *>(p.y)[m * p.ldy + n] = from_f32<T>(v);
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+        if (p.vec_y && c + 8 <= valid) {
+            *reinterpret_cast<uint4 *>(y + c) =
+                make_uint4(pack2<T>(v[c], v[c + 1]), pack2<T>(v[c + 2], v[c + 3]),
+                           pack2<T>(v[c + 4], v[c + 5]), pack2<T>(v[c + 6], v[c + 7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < valid) y[c + i] = from_f32<T>(v[c + i]);
         }
+    }
+}
+
+template <typename T, bool Gated>
+__global__ void __launch_bounds__(192, 1)
+    linear_tile_kernel(const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
+    using C = LinearTile;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_k = (p.K + C::BK - 1) / C::BK;
+    const int out_cols = Gated ? p.bn / 2 : p.bn;       // outputs a tile
+    const int b_bytes = p.bn * C::BK * 2, stage_bytes = C::A_BYTES + b_bytes;
+
+    float *bias_s = reinterpret_cast<float *>(smem + C::OFF_BIAS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + LT_COUNT);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    if (tid == 0) {
+        for (int s = 0; s < C::MAX_STAGES; ++s) {
+            mbar_init(&bars[LT_FULL + s], 1);
+            mbar_init(&bars[LT_EMPTY + s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars[LT_ACC_FULL + b], 1);
+            mbar_init(&bars[LT_ACC_EMPTY + b], 4);   // one arrival per epilogue warp
+        }
+        mbar_init(&bars[LT_DRAIN], 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == C::TMA_WARP && lane == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == C::TMA_WARP) {
+        const uint32_t leader = elect_one();
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < p.n_tiles; tile += gridDim.x) {
+            int mt, nt;
+            linear_tile_at(p, tile, mt, nt);
+            for (int ks = 0; ks < n_k; ++ks) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars[LT_EMPTY + stage], phase ^ 1, abort))) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    uint8_t *a = smem + stage * stage_bytes, *b = a + C::A_BYTES;
+                    mbar_arrive_expect_tx(&bars[LT_FULL + stage], stage_bytes);
+                    tma_load_rows(a, &tmX, &bars[LT_FULL + stage], ks * C::BK, mt * C::BM);
+                    tma_load_rows(b, &tmW, &bars[LT_FULL + stage], ks * C::BK, nt * out_cols);
+                    if (Gated)
+                        tma_load_rows(b + b_bytes / 2, &tmW, &bars[LT_FULL + stage], ks * C::BK,
+                                      p.N + nt * out_cols);
+                }
+                ++issued;
+                if (++stage == p.stages) { stage = 0; phase ^= 1; }
+            }
+        }
+        if (!ok) {
+            if (leader) give_up(abort, p.status);
+            // copies still in flight land before the CTA leaves
+            for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; ++j)
+                mbar_wait(&bars[LT_FULL + j % p.stages], (j / p.stages) & 1, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        const uint32_t leader = elect_one();
+        const uint32_t idesc = idesc_f32<T>(C::BM, 0, false, false) |
+                               (static_cast<uint32_t>(p.bn >> 3) << 17);
+        const uint64_t d0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        int stage = 0, count = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < p.n_tiles; tile += gridDim.x, ++count) {
+            const int buf = count & 1;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&bars[LT_ACC_EMPTY + buf], ((count >> 1) & 1) ^ 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + static_cast<uint32_t>(buf) * 256;
+            for (int ks = 0; ks < n_k; ++ks) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[LT_FULL + stage], phase, abort));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = d0 + static_cast<uint64_t>((stage * stage_bytes) >> 4);
+                const uint64_t bd = ad + (C::A_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < C::BK / 16; ++kk)
+                    umma_ss_w(acc, ad + kk * 2, bd + kk * 2, idesc, (ks > 0 || kk > 0) ? 1u : 0u,
+                              leader);
+                umma_commit_w(&bars[LT_EMPTY + stage], leader);
+                if (++stage == p.stages) { stage = 0; phase ^= 1; }
+            }
+            if (!ok) break;
+            umma_commit_w(&bars[LT_ACC_FULL + buf], leader);
+        }
+        if (!ok) {
+            if (leader) give_up(abort, p.status);
+            // MMAs in flight complete before the accumulators are released
+            umma_commit_w(&bars[LT_DRAIN], leader);
+            mbar_wait(&bars[LT_DRAIN], 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+        const T *bias = static_cast<const T *>(p.bias);
+        int count = 0;
+        bool ok = true;   // after a wait that gave up the warps still meet at named_sync
+        for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x, ++count) {
+            const int buf = count & 1;
+            int mt, nt;
+            linear_tile_at(p, tile, mt, nt);
+            const int row = mt * C::BM + tid, col0 = nt * out_cols;
+            named_sync(1, 128);   // the last tile's bias has been read
+            for (int c = tid; c < p.bn; c += 128) {
+                const int half = Gated && c >= out_cols;
+                const int n = col0 + c - half * out_cols;
+                bias_s[c] = bias != nullptr && n < p.N ? to_f32(bias[half * p.N + n]) : 0.0f;
+            }
+            named_sync(1, 128);
+            ok = ok && __all_sync(0xffffffffu,
+                                  mbar_wait(&bars[LT_ACC_FULL + buf], (count >> 1) & 1, abort));
+            if (!ok) {
+                if (lane == 0) give_up(abort, p.status);
+                continue;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(buf) * 256;
+#pragma unroll 1
+            for (int c = 0; c < out_cols; c += 32) {
+                uint32_t a[32];
+                float v[32];
+                tmem_ld32(acc + c, a);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]) + bias_s[c + i];
+                activate(v, p.act);
+                if constexpr (Gated) {
+                    tmem_ld32(acc + out_cols + c, a);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] *= __uint_as_float(a[i]) + bias_s[out_cols + c + i];
+                }
+                if (row < p.M && col0 + c < p.N) linear_store32<T>(p, row, col0 + c, v);
+            }
+            // accumulator reads done -> the MMA warp may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[LT_ACC_EMPTY + buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------- skinny kernel
+
+struct LinearSkinny {
+    static constexpr int BM = 128, BK = 64, MAX_COLS = 128;
+    static constexpr int W_BYTES = BM * BK * 2;
+    static constexpr int MAX_STAGES = 6;
+    static constexpr int RING_BYTES = 108 * 1024;                 // two CTAs an SM
+    static constexpr int OFF_BAR = RING_BYTES;
+    static constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;       // + alignment slack
+    static constexpr int THREADS = 192, TMA_WARP = 4, MMA_WARP = 5;
+};
+
+enum : int { LS_FULL = 0, LS_EMPTY = 6, LS_ACC = 12, LS_COUNT = 13 };
+
+// Outputs of weight row n (this thread's) for columns [c0, c0 + 16) of x rows:
+// bias, activation, gate, residual, store.
+template <typename T, bool Gated>
+__device__ __forceinline__ void linear_skinny_store(const LinearParams &p, int n, int c0,
+                                                    float (&v)[16], float (&u)[16]) {
+    const T *bias = static_cast<const T *>(p.bias), *res = static_cast<const T *>(p.residual);
+    if (bias != nullptr) {
+        const float b = to_f32(bias[n]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += b;
+    }
+    activate(v, p.act);
+    if constexpr (Gated) {
+        const float b = bias != nullptr ? to_f32(bias[p.N + n]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= u[i] + b;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (c0 + i >= p.M) break;
+        if (res != nullptr) v[i] += to_f32(res[(c0 + i) * p.ldr + n]);
+        static_cast<T *>(p.y)[(c0 + i) * p.ldy + n] = from_f32<T>(v[i]);
+    }
+}
+
+template <typename T, bool Gated>
+__global__ void __launch_bounds__(192)
+    linear_skinny_kernel(const __grid_constant__ CUtensorMap tmX,
+                         const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
+    using C = LinearSkinny;
+    constexpr int W = Gated ? 2 : 1;   // products
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
+    const int n_k = (p.K + C::BK - 1) / C::BK;
+    const int k_first = static_cast<int>(static_cast<int64_t>(n_k) * split / p.splits);
+    const int k_count = static_cast<int>(static_cast<int64_t>(n_k) * (split + 1) / p.splits) - k_first;
+    const int x_bytes = p.cols * C::BK * 2, stage_bytes = W * C::W_BYTES + x_bytes;
+    uint32_t tmem_cols = 32;
+    while (tmem_cols < static_cast<uint32_t>(W * p.cols)) tmem_cols *= 2;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + LS_COUNT);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *last_s = abort + 1;
+    if (tid == 0) {
+        for (int s = 0; s < C::MAX_STAGES; ++s) {
+            mbar_init(&bars[LS_FULL + s], 1);
+            mbar_init(&bars[LS_EMPTY + s], 1);
+        }
+        mbar_init(&bars[LS_ACC], 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(tmem_slot, tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == C::TMA_WARP) {
+        const uint32_t leader = elect_one();
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int ks = 0; ks < k_count; ++ks) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[LS_EMPTY + stage], phase ^ 1, abort));
+            if (!ok) break;
+            if (leader) {
+                uint8_t *a = smem + stage * stage_bytes;
+                const int k = (k_first + ks) * C::BK;
+                mbar_arrive_expect_tx(&bars[LS_FULL + stage], stage_bytes);
+                tma_load_rows(a, &tmW, &bars[LS_FULL + stage], k, tile * C::BM);
+                if (Gated)
+                    tma_load_rows(a + C::W_BYTES, &tmW, &bars[LS_FULL + stage], k,
+                                  p.N + tile * C::BM);
+                tma_load_rows(a + W * C::W_BYTES, &tmX, &bars[LS_FULL + stage], k, 0);
+            }
+            ++issued;
+            if (++stage == p.stages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) {
+            if (leader) give_up(abort, p.status);
+            for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; ++j)
+                mbar_wait(&bars[LS_FULL + j % p.stages], (j / p.stages) & 1, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        const uint32_t leader = elect_one();
+        const uint32_t idesc = idesc_f32<T>(C::BM, 0, false, false) |
+                               (static_cast<uint32_t>(p.cols >> 3) << 17);
+        const uint64_t d0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int ks = 0; ks < k_count; ++ks) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[LS_FULL + stage], phase, abort));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t wd = d0 + static_cast<uint64_t>((stage * stage_bytes) >> 4);
+            const uint64_t xd = wd + ((W * C::W_BYTES) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < C::BK / 16; ++kk)
+#pragma unroll
+                for (int g = 0; g < W; ++g)
+                    umma_ss_w(tmem + g * p.cols, wd + ((g * C::W_BYTES) >> 4) + kk * 2, xd + kk * 2,
+                              idesc, (ks > 0 || kk > 0) ? 1u : 0u, leader);
+            umma_commit_w(&bars[LS_EMPTY + stage], leader);
+            if (++stage == p.stages) { stage = 0; phase ^= 1; }
+        }
+        if (!ok && leader) give_up(abort, p.status);
+        // also after a wait that gave up: the MMAs in flight complete first
+        umma_commit_w(&bars[LS_ACC], leader);
+        if (!ok) mbar_wait(&bars[LS_ACC], 0, nullptr);
+        __syncwarp();
+    } else {
+        const int n = tile * C::BM + tid;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(&bars[LS_ACC], 0, abort));
+        if (!ok && lane == 0) give_up(abort, p.status);
+        tc_fence_after();
+        ok = ok && *abort == 0;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        if (p.splits == 1) {
+            for (int c = 0; ok && c < p.cols; c += 16) {
+                uint32_t a[16], b[16];
+                float v[16], u[16];
+                tmem_ld16(acc + c, a);
+                if constexpr (Gated) tmem_ld16(acc + p.cols + c, b);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[i] = __uint_as_float(a[i]);
+                    if constexpr (Gated) u[i] = __uint_as_float(b[i]);
+                }
+                if (n < p.N) linear_skinny_store<T, Gated>(p, n, c, v, u);
+            }
+        } else {
+            // every CTA leaves its part; the last one of the tile adds them up
+            const int64_t part = static_cast<int64_t>(W) * p.cols * C::BM;
+            float *mine = p.parts + (static_cast<int64_t>(tile) * p.splits + split) * part + tid;
+            for (int c = 0; ok && c < W * p.cols; c += 16) {
+                uint32_t a[16];
+                tmem_ld16(acc + c, a);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mine[(c + i) * C::BM] = __uint_as_float(a[i]);
+            }
+            __threadfence();
+            named_sync(1, 128);
+            // a CTA that gave up never arrives, so its tile is not finished by anyone
+            if (tid == 0) *last_s = *abort == 0 && atomicAdd(&p.arrived[tile], 1) == p.splits - 1;
+            named_sync(1, 128);
+            if (*last_s) {
+                __threadfence();
+                const float *all = p.parts + static_cast<int64_t>(tile) * p.splits * part + tid;
+                for (int c = 0; c < p.cols && c < p.M; c += 16) {
+                    float v[16] = {}, u[16] = {};
+                    for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v[i] += __ldcg(all + s * part + (c + i) * C::BM);
+                            if constexpr (Gated) u[i] += __ldcg(all + s * part + (p.cols + c + i) * C::BM);
+                        }
+                    }
+                    if (n < p.N) linear_skinny_store<T, Gated>(p, n, c, v, u);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, tmem_cols);
+    }
 }
 
 }  // namespace h3

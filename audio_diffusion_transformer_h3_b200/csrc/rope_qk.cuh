@@ -9,8 +9,8 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+
+#include "layer_types.cuh"
 
 namespace h3 {
 
@@ -37,14 +37,6 @@ __device__ __forceinline__ float2 rope_qk_cos_sin(int32_t position, uint64_t pha
     sincospif(x, &s, &c);
     return make_float2(a * c, a * s);
 }
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f32(float x) { return x; }
-template <typename T> __device__ __forceinline__ T from_f32(float x);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
-template <> __device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
-template <> __device__ __forceinline__ float from_f32(float x) { return x; }
 
 template <typename T>
 __global__ void __launch_bounds__(256) rope_qk_kernel(const __grid_constant__ RopeQkParams p) {
