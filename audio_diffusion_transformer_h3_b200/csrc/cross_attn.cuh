@@ -1,97 +1,735 @@
-// Packed varlen cross attention, one warp a (query token, head).
+// Packed varlen cross attention, forward, sm_100a: the queries of segment s
+// attend to the keys of segment s of another packed sequence.
+//
+// One work item is two 128-row query tiles of one segment and one key head,
+// against the segment's keys or a chunk of them. A tile's rows are (token,
+// query head) pairs of one key head's group, token by token, so that every key
+// tile is read once for the whole group; a tile of 128 rows holds 128/G tokens.
+// The kernel is persistent: a CTA per SM takes items in turn, and each role
+// walks the same list on its own, so the loads and the first score product of
+// an item run under the softmax and the output of the one before.
+//   warps 0-7   softmax, one thread a row (warpgroup t owns tile t and TMEM
+//               lanes 0..127): online softmax in the log2 domain, the running
+//               maximum m and sum l in fp32, the accumulator rescaled only when
+//               m grows by more than 2^8; P in the operands' type into the
+//               first 64 columns of S_t, in two halves of 64 keys; then O / l.
+//               Warps w and w + 4 share an SM sub-partition and take turns on
+//               its exponential unit.
+//   warp 8      tcgen05.mma issuer: S_t = Q_t K^T, O_t += P_t V.
+//   warps 9, 11 where a value tile holds rows that must not count (behind the
+//               segment's end, or masked) they write zeros over them: P is 0
+//               there, but 0 times a NaN or an infinity is not.
+//   warp 10     TMA producer.
+// A key tile's products stop at its last key (in steps of 16). Items with no
+// more rows than one tile leave the second tile out.
+//
+// Few rows: the keys of a segment are split into chunks so that all SMs read;
+// each item leaves its unnormalised O, m and l in fp32 and the last item of its
+// rows to finish joins them in the chunks' order.
+//
+// Every wait is bounded; one that gives up sets H3_ERR_DEVICE_TIMEOUT, stops
+// the CTA, and leaves TMEM and shared memory only after the copies and MMAs in
+// flight have landed.
 #pragma once
 
 #include <cstdint>
 
-#include "rope_qk.cuh"
+#include "layer_types.cuh"
 
 namespace h3 {
 
 struct CrossParams {
-    const void *q, *k, *v;
     void *o;
     float *lse;
-    int64_t ldq, ldk, ldv, ldo;
+    int64_t ldo;
     const int32_t *cu_q, *cu_k;
     const uint8_t *mask;
     int *status;
     int32_t nseg, max_q, max_k, Nq, Nk, Hq, Hk;
+    int32_t hp, tokens, heads_blocks;   // heads and tokens of a tile, Hq / hp
+    int32_t split;                      // 1: keys may be split
     float scale_log2;
+    int *arrived;                       // [item], zero at launch (split)
+    float *parts;                       // [item][slot_rows][D + 2]
+    int32_t slot_rows;
 };
 
-// Both boundary arrays, by the whole block: non-zero in every thread if bad.
-__device__ __forceinline__ int cross_bad_seqlens(const CrossParams &p) {
+constexpr int kCrossTable = 1024;       // entries of the segment table
+constexpr int kCrossItems = 296;        // items that a split aims at: two for each of 148 SMs
+constexpr int kCrossMinChunk = 2;       // key tiles of a chunk at least
+
+template <int D>
+struct CrossCfg {
+    static constexpr int NBOX = D / 64;
+    static constexpr int BOX_BYTES = 128 * 128;
+    static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
+    static constexpr int OFF_Q = 0, OFF_K = 2 * TILE_BYTES, OFF_V = 4 * TILE_BYTES;
+    static constexpr int OFF_BAR = 6 * TILE_BYTES;
+    static constexpr int OFF_TABLE = OFF_BAR + 512;
+    static constexpr int SMEM_BYTES = OFF_TABLE + (kCrossTable + 1) * 4 + 60 + 1024;
+    static constexpr uint32_t COL_S = 0, COL_O = 256;   // S_t at 128 t, O_t at 256 + 128 t
+    static constexpr int THREADS = 384;
+    // 168 registers a thread at launch; the producer warpgroup drops to 56 and
+    // the two softmax warpgroups rise to 224: 2 * 128 * 224 + 128 * 56 = 384 * 168
+    static constexpr int REGS_SOFTMAX = 224, REGS_PRODUCER = 56;
+};
+
+enum : int {
+    CB_QFULL = 0, CB_QEMPTY = 2, CB_KFULL = 4, CB_KEMPTY = 6, CB_VFULL = 8, CB_VEMPTY = 10,
+    CB_VFIX = 12, CB_SFULL = 14, CB_P1 = 16, CB_P2 = 18, CB_OFULL = 20, CB_DRAIN = 22,
+    CB_TURN = 23, CB_COUNT = 31
+};
+
+struct CrossItem {
+    int q0, q_left;      // first query token, tokens in this item (at most two tiles)
+    int head;            // block of hp query heads
+    int k0, k_left;      // first key token, keys from there to the segment's end
+    int n_kv;            // key tiles
+    int splits, group;   // chunks of these rows, item number of the first
+};
+
+struct CrossPlan {
+    const int *table;    // items before entry i, without the head blocks
+    int entries, stride; // segments an entry
+    int chunk;           // key tiles a chunk at most
+    int total;           // items
+};
+
+__device__ __forceinline__ void cross_segment(const CrossParams &p, int chunk, int s, int &blocks,
+                                              int &tiles, int &splits) {
+    const int lq = p.cu_q[s + 1] - p.cu_q[s], lk = p.cu_k[s + 1] - p.cu_k[s];
+    blocks = (lq + 2 * p.tokens - 1) / (2 * p.tokens);
+    tiles = (lk + 127) / 128;
+    splits = tiles == 0 ? 1 : (tiles + chunk - 1) / chunk;
+}
+
+__device__ __forceinline__ CrossItem cross_item(const CrossParams &p, const CrossPlan &plan, int it) {
+    const int unit = it / p.heads_blocks;
+    int lo = 0, hi = plan.entries;   // the last entry that begins at or before unit
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (plan.table[mid] <= unit) lo = mid; else hi = mid;
+    }
+    int s = lo * plan.stride, before = plan.table[lo], blocks, tiles, splits;
+    while (true) {
+        cross_segment(p, plan.chunk, s, blocks, tiles, splits);
+        if (unit < before + blocks * splits || s + 1 >= p.nseg) break;
+        before += blocks * splits;
+        ++s;
+    }
+    const int in_seg = unit - before, block = in_seg / splits, split = in_seg - block * splits;
+    const int first = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
+    CrossItem x;
+    x.head = it - unit * p.heads_blocks;
+    x.q0 = p.cu_q[s] + block * 2 * p.tokens;
+    x.q_left = min(p.cu_q[s + 1] - x.q0, 2 * p.tokens);
+    x.k0 = p.cu_k[s] + first * 128;
+    x.k_left = p.cu_k[s + 1] - x.k0;
+    x.n_kv = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits) - first;
+    x.splits = splits;
+    x.group = (before + block * splits) * p.heads_blocks + x.head;
+    return x;
+}
+
+// 3-D tile of a [N, H, D] tensor's map (dims D, H, N).
+__device__ __forceinline__ void cross_load(uint8_t *dst, const CUtensorMap *map, uint64_t *bar,
+                                           int boxes, int head, int token) {
+    for (int b = 0; b < boxes; ++b)
+        tma_load_3d(dst + b * 128 * 128, map, bar, b * 64, head, token);
+}
+
+// 2^x for two lanes on the FMA and integer pipes: x = j + f with j = rint(x)
+// and |f| <= 1/2, 2^f as a polynomial of degree 4 fitted for the least maximum
+// relative error on [-1/2, 1/2] (2.6e-6, below every rounding of P and small
+// enough for the fp32 row sums), times 2^j by the exponent field. x below -126
+// counts as -126.
+__device__ __forceinline__ void cross_exp2_fma2(float &y0, float &y1, float x0, float x1) {
+    x0 = fmaxf(x0, -126.0f);
+    x1 = fmaxf(x1, -126.0f);
+    uint32_t t0, t1, p0, p1;
+    asm("{\n\t.reg .b64 xa, ta, ra, fa, pa, sh, nsh, nm1, c0, c1, c2, c3, c4;\n\t"
+        "mov.b64 xa, {%4, %5};\n\t"
+        "mov.b64 sh, {%6, %6};\n\t"
+        "mov.b64 nsh, {%7, %7};\n\t"
+        "mov.b64 nm1, {%8, %8};\n\t"
+        "mov.b64 c0, {%9, %9};\n\t"
+        "mov.b64 c1, {%10, %10};\n\t"
+        "mov.b64 c2, {%11, %11};\n\t"
+        "mov.b64 c3, {%12, %12};\n\t"
+        "mov.b64 c4, {%13, %13};\n\t"
+        "add.rn.f32x2 ta, xa, sh;\n\t"
+        "add.rn.f32x2 ra, ta, nsh;\n\t"
+        "fma.rn.f32x2 fa, ra, nm1, xa;\n\t"
+        "fma.rn.f32x2 pa, c4, fa, c3;\n\t"
+        "fma.rn.f32x2 pa, pa, fa, c2;\n\t"
+        "fma.rn.f32x2 pa, pa, fa, c1;\n\t"
+        "fma.rn.f32x2 pa, pa, fa, c0;\n\t"
+        "mov.b64 {%0, %1}, ta;\n\t"
+        "mov.b64 {%2, %3}, pa;\n\t}"
+        : "=r"(t0), "=r"(t1), "=r"(p0), "=r"(p1)
+        : "f"(x0), "f"(x1), "f"(12582912.0f), "f"(-12582912.0f), "f"(-1.0f),
+          "f"(0.9999992847442627f), "f"(0.6931217908859253f), "f"(0.240247443318367f),
+          "f"(0.05591786280274391f), "f"(0.009570102207362652f));
+    y0 = __uint_as_float(t0 * 8388608u + p0);
+    y1 = __uint_as_float(t1 * 8388608u + p1);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(384, 1)
+    cross_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const CrossParams p) {
+    using C = CrossCfg<D>;
+    // fp16: P is scaled by 2^6 so that values down to 2^-20 of the row's
+    // largest stay normal; with the 2^8 of slack the largest is 2^14
+    constexpr float P_SHIFT = std::is_same<T, __half>::value ? 6.0f : 0.0f;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + CB_COUNT);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *last_s = abort + 1;                                     // [2]
+    unsigned long long *units_s = reinterpret_cast<unsigned long long *>(bars + CB_COUNT + 3);
+    int *table = reinterpret_cast<int *>(smem + C::OFF_TABLE);
+
+    // ---- the boundaries, checked by every CTA; the work they make
+    CrossPlan plan;
+    plan.stride = (p.nseg + kCrossTable - 1) / kCrossTable;
+    plan.entries = (p.nseg + plan.stride - 1) / plan.stride;
+    plan.table = table;
+    plan.chunk = 1 << 24;   // more than any segment has: no split
+    if (tid == 0) *units_s = 0;
     int bad = 0;
-    for (int i = threadIdx.x; i <= p.nseg; i += blockDim.x) {
+    unsigned long long units = 0;
+    for (int i = tid; i <= p.nseg; i += C::THREADS) {
         const int a = p.cu_q[i], b = p.cu_k[i];
         if (i == 0 && (a != 0 || b != 0)) bad = 1;
         if (i == p.nseg && (a > p.Nq || b > p.Nk)) bad = 1;
         if (i > 0) {
             const int pa = p.cu_q[i - 1], pb = p.cu_k[i - 1];
             if (a < pa || a - pa > p.max_q || b < pb || b - pb > p.max_k) bad = 1;
+            units += static_cast<unsigned long long>((a - pa + 2 * p.tokens - 1) / (2 * p.tokens)) *
+                     static_cast<unsigned>((b - pb + 127) / 128);
         }
     }
-    return __syncthreads_or(bad);
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(128) cross_attn_kernel(const CrossParams p) {
-    __shared__ float qs[4][D];
-    if (cross_bad_seqlens(p)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(p.status, 0, 7);
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && blockIdx.x == 0) atomicCAS(p.status, 0, 7);
         return;
     }
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int total = p.cu_q[p.nseg];
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + warp;
-         at < static_cast<int64_t>(total) * p.Hq; at += static_cast<int64_t>(gridDim.x) * 4) {
-        const int row = static_cast<int>(at / p.Hq), head = static_cast<int>(at % p.Hq);
-        const int kvh = head / (p.Hq / p.Hk);
-        int lo = 0, hi = p.nseg;   // last segment that begins at or before row and holds it
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (p.cu_q[mid] <= row) lo = mid; else hi = mid;
+    if (p.split) {
+        if (units) atomicAdd(units_s, units);
+        __syncthreads();
+        const unsigned long long all = *units_s * static_cast<unsigned>(p.heads_blocks);
+        plan.chunk = static_cast<int>(max((all + kCrossItems - 1) / kCrossItems,
+                                          static_cast<unsigned long long>(kCrossMinChunk)));
+    }
+    for (int e = tid; e < plan.entries; e += C::THREADS) {
+        int sum = 0;
+        for (int s = e * plan.stride; s < min((e + 1) * plan.stride, p.nseg); ++s) {
+            int blocks, tiles, splits;
+            cross_segment(p, plan.chunk, s, blocks, tiles, splits);
+            sum += blocks * splits;
         }
-        const int k0 = p.cu_k[lo], k1 = p.cu_k[lo + 1];
-        __syncwarp();
-        for (int d = lane; d < D; d += 32)
-            qs[warp][d] = to_f32(static_cast<const T *>(p.q)[row * p.ldq + head * D + d]);
-        __syncwarp();
-        float m = -INFINITY, l = 0.0f, acc[D / 32] = {};
-        for (int j0 = k0; j0 < k1; j0 += 32) {
-            const int j = j0 + lane;
-            float s = -INFINITY;
-            if (j < k1 && (p.mask == nullptr || p.mask[j] != 0)) {
-                const T *kr = static_cast<const T *>(p.k) + j * p.ldk + kvh * D;
-                float dot = 0.0f;
-                for (int d = 0; d < D; ++d) dot = fmaf(qs[warp][d], to_f32(kr[d]), dot);
-                s = dot * p.scale_log2;
+        table[e + 1] = sum;
+    }
+    if (tid == 0) {
+        table[0] = 0;
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars[CB_QFULL + s], 1);
+            mbar_init(&bars[CB_QEMPTY + s], 1);
+            mbar_init(&bars[CB_KFULL + s], 1);
+            mbar_init(&bars[CB_KEMPTY + s], 2);   // one commit for each tile
+            mbar_init(&bars[CB_VFULL + s], 1);
+            mbar_init(&bars[CB_VEMPTY + s], 2);
+            mbar_init(&bars[CB_VFIX + s], 2);     // warps 9 and 11
+            mbar_init(&bars[CB_SFULL + s], 1);
+            mbar_init(&bars[CB_P1 + s], 4);
+            mbar_init(&bars[CB_P2 + s], 4);
+            mbar_init(&bars[CB_OFULL + s], 1);
+        }
+        mbar_init(&bars[CB_DRAIN], 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&bars[CB_TURN + i], 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == 10 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    __syncthreads();
+    if (warp == 0) {   // running sums of the table
+        int carry = 0;
+        for (int e = 0; e < plan.entries; e += 32) {
+            int x = e + lane < plan.entries ? table[e + lane + 1] : 0;
+            for (int d = 1; d < 32; d *= 2) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
             }
-            const unsigned kept = __ballot_sync(0xffffffffu, s != -INFINITY);
-            if (kept == 0) continue;
-            float mx = s;
-            for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(mx, m);
-            const float f = exp2f(m - mx), e = s == -INFINITY ? 0.0f : exp2f(s - mx);
-            m = mx;
-            float sum = e;
-            for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = l * f + sum;
-            for (int c = 0; c < D / 32; ++c) acc[c] *= f;
-            for (int i = 0; i < 32; ++i) {
-                const float pi = __shfl_sync(0xffffffffu, e, i);
-                if (!((kept >> i) & 1)) continue;
-                const T *vr = static_cast<const T *>(p.v) + (j0 + i) * p.ldv + kvh * D;
-                for (int c = 0; c < D / 32; ++c)
-                    acc[c] = fmaf(pi, to_f32(vr[c * 32 + lane]), acc[c]);
+            x += carry;
+            if (e + lane < plan.entries) table[e + lane + 1] = x;
+            carry = __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    plan.total = table[plan.entries] * p.heads_blocks;
+
+    // keys of a key tile, and its MMA steps of 16 keys
+    auto keys_in = [](const CrossItem &x, int j) { return min(x.k_left - j * 128, 128); };
+
+    if (warp == 10) {
+        // ============================ TMA producer ============================
+        reg_dealloc<C::REGS_PRODUCER>();
+        const uint32_t leader = elect_one();
+        const uint32_t q_bytes = static_cast<uint32_t>(C::NBOX * 128 * p.hp * p.tokens);
+        auto wait = [&](int bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort));
+        };
+        int nq[2] = {0, 0}, nk = 0, nv = 0;   // loads issued
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < plan.total; it += gridDim.x) {
+            const CrossItem x = cross_item(p, plan, it);
+            if (x.n_kv == 0) continue;
+            const int kv_head = x.head * p.hp / (p.Hq / p.Hk);
+            const int n_t = x.q_left > p.tokens ? 2 : 1;
+            for (int j = 0; ok && j < x.n_kv; ++j) {
+                if (j == 0)
+                    for (int t = 0; ok && t < n_t; ++t) {
+                        ok = wait(CB_QEMPTY + t, (nq[t] & 1) ^ 1);
+                        if (!ok) break;
+                        if (leader) {
+                            mbar_arrive_expect_tx(&bars[CB_QFULL + t], q_bytes);
+                            cross_load(smem + C::OFF_Q + t * C::TILE_BYTES, &tmQ,
+                                       &bars[CB_QFULL + t], C::NBOX, x.head * p.hp,
+                                       x.q0 + t * p.tokens);
+                        }
+                        ++nq[t];
+                    }
+                if (!ok) break;
+                const int s = nk & 1;
+                ok = wait(CB_KEMPTY + s, ((nk >> 1) & 1) ^ 1);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(&bars[CB_KFULL + s], C::TILE_BYTES);
+                    cross_load(smem + C::OFF_K + s * C::TILE_BYTES, &tmK, &bars[CB_KFULL + s],
+                               C::NBOX, kv_head, x.k0 + j * 128);
+                }
+                ++nk;
+                ok = wait(CB_VEMPTY + s, ((nv >> 1) & 1) ^ 1);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(&bars[CB_VFULL + s], C::TILE_BYTES);
+                    cross_load(smem + C::OFF_V + s * C::TILE_BYTES, &tmV, &bars[CB_VFULL + s],
+                               C::NBOX, kv_head, x.k0 + j * 128);
+                }
+                ++nv;
             }
         }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        T *orow = static_cast<T *>(p.o) + row * p.ldo + head * D;
-        for (int c = 0; c < D / 32; ++c) orow[c * 32 + lane] = from_f32<T>(acc[c] * inv);
-        if (p.lse != nullptr && lane == 0)
-            p.lse[static_cast<int64_t>(head) * p.Nq + row] =
-                l > 0.0f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+        if (!ok && leader) give_up(abort, p.status);
+        if (*abort) {
+            // the copies still in flight land before shared memory is released
+            for (int t = 0; t < 2; ++t)
+                if (nq[t] > 0) mbar_wait(&bars[CB_QFULL + t], (nq[t] - 1) & 1, nullptr);
+            for (int j = max(nk - 2, 0); j < nk; ++j)
+                mbar_wait(&bars[CB_KFULL + (j & 1)], (j >> 1) & 1, nullptr);
+            for (int j = max(nv - 2, 0); j < nv; ++j)
+                mbar_wait(&bars[CB_VFULL + (j & 1)], (j >> 1) & 1, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 9 || warp == 11) {
+        // ============================ value rows that must not count ==========
+        reg_dealloc<C::REGS_PRODUCER>();
+        const int half = warp == 11;
+        int nv = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < plan.total; it += gridDim.x) {
+            const CrossItem x = cross_item(p, plan, it);
+            for (int j = 0; ok && j < x.n_kv; ++j, ++nv) {
+                const int keys = keys_in(x, j), s = nv & 1, rows = (keys + 15) / 16 * 16;
+                // every phase is waited for, those of tiles that need nothing too: a
+                // parity tells a phase from its neighbours only
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars[CB_VFULL + s], (nv >> 1) & 1, abort));
+                if (!ok) break;
+                if (p.mask == nullptr && keys % 16 == 0) continue;
+                uint8_t *v = smem + C::OFF_V + s * C::TILE_BYTES;
+                // four rows a step, eight lanes a row; warp 9 the even fours
+                for (int r0 = half * 4; r0 < rows; r0 += 8) {
+                    const int r = r0 + lane / 8;
+                    const bool counts = r < keys &&
+                        (p.mask == nullptr || p.mask[x.k0 + j * 128 + r] != 0);
+                    if (!counts && r < rows)
+                        for (int b = 0; b < C::NBOX; ++b)
+                            *reinterpret_cast<uint4 *>(v + b * C::BOX_BYTES + r * 128 +
+                                                       (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[CB_VFIX + s]);
+            }
+        }
+        if (!ok && lane == 0) give_up(abort, p.status);
+    } else if (warp == 8) {
+        // ============================ MMA issuer ==============================
+        reg_dealloc<C::REGS_PRODUCER>();
+        const uint32_t leader = elect_one();
+        constexpr uint32_t IDESC_S = idesc_f32<T>(128, 0, false, false);
+        constexpr uint32_t IDESC_O = idesc_f32<T>(128, D, false, true);
+        const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+        const uint64_t dK = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+        const uint64_t dV = sdesc_sw128(smem_u32(smem + C::OFF_V), C::BOX_BYTES, 1024);
+        auto wait = [&](int bar, uint32_t parity) {
+            const bool r = __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort));
+            tc_fence_after();
+            return r;
+        };
+        auto issue_s = [&](int t, int stage, int keys) {
+            const uint32_t n16 = static_cast<uint32_t>((keys + 15) / 16);
+            const uint64_t dq = dQ + static_cast<uint64_t>((t * C::TILE_BYTES) >> 4);
+            const uint64_t dk = dK + static_cast<uint64_t>((stage * C::TILE_BYTES) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::BOX_BYTES + (kk & 3) * 32) >> 4;
+                umma_ss_w(tmem + C::COL_S + t * 128, dq + off, dk + off, IDESC_S | ((n16 * 2) << 17),
+                          kk > 0 ? 1u : 0u, leader);
+            }
+        };
+        auto issue_pv = [&](int t, int stage, int from, int to, bool add) {
+            const uint64_t dv = dV + static_cast<uint64_t>((stage * C::TILE_BYTES) >> 4);
+            for (int kk = from; kk < to; ++kk)
+                umma_ts_w(tmem + C::COL_O + t * 128, tmem + C::COL_S + t * 128 + kk * 8,
+                          dv + static_cast<uint64_t>((kk * 2048) >> 4), IDESC_O,
+                          (add || kk > 0) ? 1u : 0u, leader);
+        };
+        int nq[2] = {0, 0}, g[2] = {0, 0};   // items and key tiles of each query tile so far
+        int nkv = 0;                         // key tiles so far
+        uint32_t fixes = 0;                  // parity of the next VFIX phase, a bit a stage
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < plan.total; it += gridDim.x) {
+            const CrossItem x = cross_item(p, plan, it);
+            if (x.n_kv == 0) continue;
+            const int n_t = x.q_left > p.tokens ? 2 : 1;
+            for (int t = 0; ok && t < n_t; ++t) {
+                ok = wait(CB_QFULL + t, nq[t] & 1) && wait(CB_KFULL + (nkv & 1), (nkv >> 1) & 1);
+                if (!ok) break;
+                issue_s(t, nkv & 1, keys_in(x, 0));
+                umma_commit_w(&bars[CB_SFULL + t], leader);
+                umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
+                if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
+                if (x.n_kv == 1) umma_commit_w(&bars[CB_QEMPTY + t], leader);
+                ++nq[t];
+            }
+            for (int j = 0; ok && j < x.n_kv; ++j, ++nkv) {
+                const int s = nkv & 1, keys = keys_in(x, j), n16 = (keys + 15) / 16;
+                const bool more = j + 1 < x.n_kv, fix = p.mask != nullptr || keys % 16 != 0;
+                for (int t = 0; ok && t < n_t; ++t) {
+                    ok = wait(CB_P1 + t, g[t] & 1) && wait(CB_VFULL + s, (nkv >> 1) & 1);
+                    if (ok && fix && t == 0) ok = wait(CB_VFIX + s, (fixes >> s) & 1);
+                    if (!ok) break;
+                    issue_pv(t, s, 0, min(n16, 4), j > 0);
+                    ok = wait(CB_P2 + t, g[t] & 1);
+                    if (!ok) break;
+                    issue_pv(t, s, 4, n16, true);
+                    umma_commit_w(&bars[CB_VEMPTY + s], leader);
+                    if (n_t == 1) umma_commit_w(&bars[CB_VEMPTY + s], leader);
+                    if (more) {
+                        const int s1 = (nkv + 1) & 1;
+                        ok = wait(CB_KFULL + s1, ((nkv + 1) >> 1) & 1);
+                        if (!ok) break;
+                        issue_s(t, s1, keys_in(x, j + 1));
+                        umma_commit_w(&bars[CB_SFULL + t], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + s1], leader);
+                        if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + s1], leader);
+                        if (j + 2 == x.n_kv) umma_commit_w(&bars[CB_QEMPTY + t], leader);
+                    } else {
+                        umma_commit_w(&bars[CB_OFULL + t], leader);
+                    }
+                    ++g[t];
+                }
+                if (fix) fixes ^= 1u << s;
+            }
+        }
+        if (!ok) {
+            if (leader) give_up(abort, p.status);
+            umma_commit_w(&bars[CB_DRAIN], leader);
+            mbar_wait(&bars[CB_DRAIN], 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ============================ softmax / output ========================
+        reg_alloc<C::REGS_SOFTMAX>();
+        const int t = warp >> 2;                 // query tile of this warpgroup
+        const int r = tid & 127;                 // row of the tile = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + C::COL_S + t * 128;
+        const uint32_t tO = tmem + lane_off + C::COL_O + t * 128;
+        const float sl2 = p.scale_log2;
+        auto wait = [&](int bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort));
+        };
+        int items = 0, g = 0, turns = 0;   // of this tile: items, key tiles, key tiles in turn
+        // after a wait that gave up, the warps go on to meet at named_sync
+        bool ok = true;
+        for (int it = blockIdx.x; it < plan.total; it += gridDim.x) {
+            const CrossItem x = cross_item(p, plan, it);
+            const bool two = x.q_left > p.tokens;
+            if (t == 1 && !two) continue;
+            const int rows = min(x.q_left - t * p.tokens, p.tokens) * p.hp;
+            const bool active = (warp & 3) * 32 < rows;   // a warp without rows only signals
+            const bool row_ok = r < rows;
+            const int tok = r / p.hp;
+            const int qrow = x.q0 + t * p.tokens + tok, head = x.head * p.hp + r - tok * p.hp;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; ok && j < x.n_kv; ++j, ++g) {
+                const int keys = keys_in(x, j);
+                uint32_t valid[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                const bool part = keys < 128 || p.mask != nullptr;
+                if (part) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = i * 32 + lane;
+                        valid[i] = __ballot_sync(0xffffffffu, c < keys &&
+                            (p.mask == nullptr || p.mask[x.k0 + j * 128 + c] != 0));
+                    }
+                }
+                ok = wait(CB_SFULL + t, g & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const bool none = (valid[0] | valid[1] | valid[2] | valid[3]) == 0;
+                if (!active || none) {
+                    if (active) {
+                        uint32_t z[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) z[i] = 0u;
+                        tmem_st32(tS + 0, z);
+                        tmem_st32(tS + 32, z);
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (two) {
+                        if (t == 1 || turns > 0)
+                            ok = wait(t == 0 ? CB_TURN + (warp & 3) : CB_TURN + 4 + (warp & 3),
+                                      static_cast<uint32_t>(t == 0 ? (turns - 1) & 1 : turns & 1));
+                        if (!ok) break;
+                        ++turns;
+                        if (lane == 0)
+                            mbar_arrive(&bars[t == 0 ? CB_TURN + 4 + (warp & 3) : CB_TURN + (warp & 3)]);
+                    }
+                    if (lane == 0) {
+                        mbar_arrive(&bars[CB_P1 + t]);
+                        mbar_arrive(&bars[CB_P2 + t]);
+                    }
+                    continue;
+                }
+                const bool long_tile = keys > 64;
+                uint32_t s[128];
+                tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                if (long_tile) {
+                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                }
+                tmem_wait_ld();
+                if (part) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (!((valid[c >> 5] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+                }
+                float mq[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mq[i] = __uint_as_float(s[i]);
+#pragma unroll
+                for (int c = 8; c < 56; c += 16)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mq[i] = fmax3(mq[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mq[i] = fmaxf(mq[i], __uint_as_float(s[56 + i]));
+                if (long_tile) {
+#pragma unroll
+                    for (int c = 64; c < 128; c += 16)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mq[i] = fmax3(mq[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
+                }
+                const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
+                                       fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
+                const float m_new = mx * sl2;
+                // the accumulator holds something from the item's second key tile on
+                const bool grow = m_new > m + 8.0f || m == -INFINITY;
+                const bool need = grow && j > 0;
+                const float f = need ? ex2_approx(m - m_new) : 1.0f;
+                if (grow) {
+                    l *= need ? f : 0.0f;
+                    m = m_new;
+                }
+                const float nm = P_SHIFT - m;
+                uint32_t pk[64];
+                uint64_t acc0 = 0, acc1 = 0;
+                const uint64_t s2 = f2_splat(sl2), n2 = f2_splat(nm);
+                // P of keys [64 h, 64 h + 64), three pairs of eight on the FMA pipe
+                auto exp_half = [&](const int h) {
+#pragma unroll
+                    for (int c = 32 * h; c < 32 * h + 32; ++c) {
+                        float x0, x1, p0, p1;
+                        ffma2(x0, x1, __uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), s2, n2);
+                        if ((c & 7) >= 5) {
+                            cross_exp2_fma2(p0, p1, x0, x1);
+                        } else {
+                            p0 = ex2_approx(x0);
+                            p1 = ex2_approx(x1);
+                        }
+                        if (c & 1) fadd2(acc1, p0, p1); else fadd2(acc0, p0, p1);
+                        pk[c] = pack2<T>(p0, p1);
+                    }
+                };
+                if (two && (t == 1 || turns > 0)) {
+                    ok = wait(t == 0 ? CB_TURN + (warp & 3) : CB_TURN + 4 + (warp & 3),
+                              static_cast<uint32_t>(t == 0 ? (turns - 1) & 1 : turns & 1));
+                    if (!ok) break;
+                }
+                exp_half(0);
+                tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                if (__any_sync(0xffffffffu, need)) {
+                    // O holds P V up to the tile before; rescale it before P is released
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(tO + c * 32, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[CB_P1 + t]);
+                if (long_tile) exp_half(1);
+                if (two) {
+                    ++turns;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars[t == 0 ? CB_TURN + 4 + (warp & 3) : CB_TURN + (warp & 3)]);
+                }
+                l += f2_sum(acc0) + f2_sum(acc1);
+                if (long_tile) {
+                    tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[CB_P2 + t]);
+            }
+            if (x.n_kv > 0) {
+                ok = ok && wait(CB_OFULL + t, items & 1);
+                ++items;
+                tc_fence_after();
+            }
+            if (!ok && lane == 0) give_up(abort, p.status);
+            if (x.splits == 1) {
+                if (!ok || !active) continue;
+                const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
+                uint4 *orow = reinterpret_cast<uint4 *>(
+                    static_cast<T *>(p.o) + qrow * p.ldo + static_cast<int64_t>(head) * D);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (x.n_kv > 0) tmem_ld32(tO + c * 32, o);
+                    tmem_wait_ld();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = l > 0.0f ? pack2<T>(__uint_as_float(o[2 * i]) * inv_l,
+                                                   __uint_as_float(o[2 * i + 1]) * inv_l) : 0u;
+                    if (row_ok) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            orow[c * 4 + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    }
+                }
+                if (row_ok && p.lse != nullptr)
+                    p.lse[static_cast<int64_t>(head) * p.Nq + qrow] =
+                        l > 0.0f ? (m + (log2f(l) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
+                continue;
+            }
+            // ---- one chunk of the keys: leave O, m, l; the rows' last item joins
+            const int64_t slot = static_cast<int64_t>(p.slot_rows) * (D + 2);
+            const int row0 = t * p.tokens * p.hp;     // of this tile in the slot
+            if (ok && active) {
+                float *mine = p.parts + it * slot + static_cast<int64_t>(row0 + r) * (D + 2);
+                if (row_ok) *reinterpret_cast<float2 *>(mine) = make_float2(m, l);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c * 32, o);
+                    tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            *reinterpret_cast<uint2 *>(mine + 2 + c * 32 + i) = make_uint2(o[i], o[i + 1]);
+                    }
+                }
+            }
+            __threadfence();
+            // the two tiles of an item may be at different items: a count and a flag each
+            named_sync(1 + t, 128);
+            if (r == 0)
+                last_s[t] = *abort == 0 &&
+                            atomicAdd(&p.arrived[2 * x.group + t], 1) == x.splits - 1;
+            named_sync(1 + t, 128);
+            if (!last_s[t]) continue;
+            __threadfence();
+            for (int rr = warp & 3; rr < rows; rr += 4) {   // a warp a row
+                const float *all = p.parts + x.group * slot + static_cast<int64_t>(row0 + rr) * (D + 2);
+                const int64_t step = slot * p.heads_blocks;
+                float mm = -INFINITY;
+                for (int i = 0; i < x.splits; ++i) mm = fmaxf(mm, __ldcg(all + i * step));
+                float sum = 0.0f, o[D / 32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
+                for (int i = 0; i < x.splits; ++i) {
+                    const float mi = __ldcg(all + i * step);
+                    const float wgt = mi == -INFINITY ? 0.0f : ex2_approx(mi - mm);
+                    sum = fmaf(wgt, __ldcg(all + i * step + 1), sum);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(
+                            all + i * step + 2 + c * 64 + lane * 2));
+                        o[2 * c] = fmaf(wgt, v.x, o[2 * c]);
+                        o[2 * c + 1] = fmaf(wgt, v.y, o[2 * c + 1]);
+                    }
+                }
+                const int rt = rr / p.hp;
+                const int row = x.q0 + t * p.tokens + rt, hh = x.head * p.hp + rr - rt * p.hp;
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                T *orow = static_cast<T *>(p.o) + row * p.ldo + static_cast<int64_t>(hh) * D;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    *reinterpret_cast<uint32_t *>(orow + c * 64 + lane * 2) =
+                        pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
+                if (lane == 0 && p.lse != nullptr)
+                    p.lse[static_cast<int64_t>(hh) * p.Nq + row] =
+                        sum > 0.0f ? (mm + (log2f(sum) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 

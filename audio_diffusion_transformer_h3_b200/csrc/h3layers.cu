@@ -219,12 +219,69 @@ bool cross_sizes_ok(int64_t Nq, int64_t Nk, int32_t Hq, int32_t Hk, int32_t nseg
            Hq >= Hk && Hq <= 65535 && Hq % Hk == 0 && nseg >= 1 && nseg <= 65535;
 }
 
-template <typename T>
-void launch_cross(const h3::CrossParams &p, int D, int sms, cudaStream_t st) {
-    const int64_t blocks = (static_cast<int64_t>(p.Nq) * p.Hq + 3) / 4;
-    const int grid = static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 64));
-    if (D == 128) h3::cross_attn_kernel<T, 128><<<grid, 128, 0, st>>>(p);
-    else h3::cross_attn_kernel<T, 64><<<grid, 128, 0, st>>>(p);
+struct CrossPlanHost {
+    int32_t hp, tokens;       // heads and tokens of a 128-row tile
+    int64_t items;            // bound on the items without a split
+    bool split;
+    int64_t slots;            // bound on the items with it
+    int32_t slot_rows;
+};
+
+// A tile takes the whole group of query heads of a key head where the group
+// fits, else single heads. The keys are split where the items alone could not
+// give each SM two and a segment may have more key tiles than a chunk has.
+CrossPlanHost cross_plan(int64_t Nq, int32_t Hq, int32_t Hk, int32_t nseg, int32_t max_q,
+                         int32_t max_k) {
+    CrossPlanHost c;
+    const int32_t group = Hq / Hk;
+    c.hp = group <= 128 ? group : 1;
+    c.tokens = 128 / c.hp;
+    const int64_t two = 2 * c.tokens;
+    c.items = std::min(nseg * ((max_q + two - 1) / two), Nq / two + nseg) * (Hq / c.hp);
+    c.split = c.items < h3::kCrossItems && (static_cast<int64_t>(max_k) + 127) / 128 > h3::kCrossMinChunk;
+    c.slots = c.split ? c.items + h3::kCrossItems : 0;
+    c.slot_rows = static_cast<int32_t>(std::min<int64_t>(two, max_q)) * c.hp;
+    return c;
+}
+
+size_t cross_counter_bytes(const CrossPlanHost &c) {
+    return h3host::round_up(static_cast<size_t>(c.slots) * 8, 256);
+}
+
+// TMA map over a [N, H, D] tensor of 16-bit elements, token stride ld, box
+// 64 channels x `heads` x `tokens`, 128-byte swizzle, zeros out of bounds.
+h3_status make_heads_map(CUtensorMap *map, const void *base, int64_t N, int32_t H, int32_t D,
+                         int64_t ld, uint32_t heads, uint32_t tokens) {
+    const h3host::EncodeTiledFn enc = h3host::encode_tiled();
+    if (enc == nullptr) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                                static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[3] = {64, heads, tokens};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims,
+                           strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? H3_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+template <typename T, int D>
+h3_status launch_cross(const h3::CrossParams &p, int grid, const CUtensorMap &tq,
+                       const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
+    using C = h3::CrossCfg<D>;
+    const auto kernel = h3::cross_attn_kernel<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::SMEM_BYTES);
+    // the softmax warpgroups' raise waits for registers that the block holds
+    // from launch: a build whose launch allocation does not cover it is refused
+    cudaFuncAttributes a{};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (a.numRegs * C::THREADS < 2 * 128 * C::REGS_SOFTMAX + 128 * C::REGS_PRODUCER)
+        return H3_ERR_UNSUPPORTED;
+    kernel<<<grid, C::THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
+    return launched();
 }
 
 }  // namespace
@@ -361,7 +418,9 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
                                int32_t max_q, int32_t max_k) {
     if (!cross_sizes_ok(Nq, 0, Hq, Hk, nseg) || (D != 64 && D != 128) || max_q < 0 || max_k < 0)
         return 0;
-    return kStatusBytes;
+    const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
+    return kStatusBytes + cross_counter_bytes(c) +
+           static_cast<size_t>(c.slots) * c.slot_rows * (D + 2) * 4;
 }
 
 h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk,
@@ -397,21 +456,41 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     h3_status st = device_info(&d);
     if (st != H3_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), cs);
+    const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const cudaError_t e = cudaMemsetAsync(
+        ws, 0, Nq > 0 && c.split ? kStatusBytes + cross_counter_bytes(c) : sizeof(int), cs);
     if (e != cudaSuccess) return cuda_fail(e);
     if (Nq == 0) return H3_OK;
     h3::CrossParams p;
-    p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse;
-    p.ldq = ldq; p.ldk = ldk; p.ldv = ldv; p.ldo = ldo;
+    std::memset(&p, 0, sizeof(p));
+    p.o = o; p.lse = lse; p.ldo = ldo;
     p.cu_q = cu_q; p.cu_k = cu_k; p.mask = key_mask;
-    p.status = static_cast<int *>(workspace);
+    p.status = reinterpret_cast<int *>(ws);
     p.nseg = nseg; p.max_q = max_q; p.max_k = max_k;
     p.Nq = static_cast<int32_t>(Nq); p.Nk = static_cast<int32_t>(Nk);
     p.Hq = Hq; p.Hk = Hk;
-    p.scale_log2 = softmax_scale * 1.4426950408889634f;
-    if (dtype == H3_BF16) launch_cross<__nv_bfloat16>(p, D, d->sms, cs);
-    else launch_cross<__half>(p, D, d->sms, cs);
-    return launched();
+    p.hp = c.hp; p.tokens = c.tokens; p.heads_blocks = Hq / c.hp;
+    p.split = c.split;
+    // a scale of 0 (the mean of the values) as one that no score survives, so
+    // that a masked score of -infinity stays one
+    p.scale_log2 = std::max(softmax_scale * 1.4426950408889634f, 1e-30f);
+    p.arrived = reinterpret_cast<int *>(ws + kStatusBytes);
+    p.parts = reinterpret_cast<float *>(ws + kStatusBytes + cross_counter_bytes(c));
+    p.slot_rows = c.slot_rows;
+    CUtensorMap tq, tk, tv;
+    if ((st = make_heads_map(&tq, q, Nq, Hq, D, ldq, c.hp, c.tokens)) != H3_OK) return st;
+    // without keys nothing is loaded: any valid map will do
+    if ((st = Nk > 0 ? make_heads_map(&tk, k, Nk, Hk, D, ldk, 1, 128)
+                     : make_heads_map(&tk, q, Nq, Hq, D, ldq, 1, 128)) != H3_OK) return st;
+    if ((st = Nk > 0 ? make_heads_map(&tv, v, Nk, Hk, D, ldv, 1, 128)
+                     : make_heads_map(&tv, q, Nq, Hq, D, ldq, 1, 128)) != H3_OK) return st;
+    const int grid = static_cast<int>(std::min<int64_t>(d->sms, c.items + c.slots));
+    if (dtype == H3_BF16)
+        return D == 128 ? launch_cross<__nv_bfloat16, 128>(p, grid, tq, tk, tv, cs)
+                        : launch_cross<__nv_bfloat16, 64>(p, grid, tq, tk, tv, cs);
+    return D == 128 ? launch_cross<__half, 128>(p, grid, tq, tk, tv, cs)
+                    : launch_cross<__half, 64>(p, grid, tq, tk, tv, cs);
 }
 
 }  // extern "C"
