@@ -605,6 +605,12 @@ def _on(device, stream):
     return torch.cuda.stream(stream)
 
 
+def _current_stream(device) -> int:
+    """Handle of the device's current stream, without building a stream object."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _heads(x, name):
     """(token stride) of a [N, H, D] tensor whose heads are contiguous."""
     if x.dim() != 3:
@@ -676,8 +682,8 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
             raise ValueError("k must be [N, Hk, D] of q's type")
         Hk, ldk, kp = k.shape[1], _heads(k, "k"), k.data_ptr()
     if out is None:
-        qo = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty((N, Hk, D), dtype=q.dtype, device=q.device)
+        qo = q.new_empty((N, Hq, D))
+        ko = None if k is None else q.new_empty((N, Hk, D))
         ldqo, ldko = Hq * D, Hk * D
     else:
         qo, ko = out
@@ -688,7 +694,7 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
         ldqo, ldko = _heads(qo, "q_out"), 0 if ko is None else _heads(ko, "k_out")
     _check(h3_rope_qk_apply(q.data_ptr(), ldq, qo.data_ptr(), ldqo, kp, ldk,
                             0 if ko is None else ko.data_ptr(), ldko, positions.data_ptr(), cfg,
-                            N, Hq, Hk, D, code, torch.cuda.current_stream().cuda_stream),
+                            N, Hq, Hk, D, code, _current_stream(q.device)),
            "h3_rope_qk_apply")
     return qo, ko
 
@@ -734,7 +740,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
             raise ValueError(f"residual must be [{M}, {N}] of x's type")
         ldr = _rows(residual, "residual")
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, N))
     elif out.shape != (M, N) or out.dtype != x.dtype:
         raise ValueError(f"out must be [{M}, {N}] of x's type")
     if workspace is None:
@@ -743,7 +749,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
                          0 if bias is None else bias.data_ptr(),
                          0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
                          _rows(out, "out"), M, N, K, a, code, workspace.data_ptr(),
-                         workspace.numel(), torch.cuda.current_stream().cuda_stream),
+                         workspace.numel(), _current_stream(x.device)),
            "h3_linear_fwd")
     return out
 
@@ -787,7 +793,7 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                                  key_mask.dtype not in (torch.bool, torch.uint8)):
         raise ValueError(f"key_mask must be contiguous bool or uint8 [{Nk}]")
     if out is None:
-        out = torch.empty((Nq, Hq, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty((Nq, Hq, D))
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
     lse = torch.empty((Hq, Nq), dtype=torch.float32, device=q.device) if return_lse else None
@@ -800,6 +806,6 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                              cu_k.data_ptr(), nseg, int(max_q), int(max_k),
                              0 if key_mask is None else key_mask.data_ptr(), Nq, Nk, Hq, Hk, D,
                              scale, code, workspace.data_ptr(), workspace.numel(),
-                             torch.cuda.current_stream().cuda_stream),
+                             _current_stream(q.device)),
            "h3_cross_attn_fwd")
     return (out, lse) if return_lse else out

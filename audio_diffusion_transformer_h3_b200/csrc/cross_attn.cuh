@@ -5,9 +5,9 @@
 // against the segment's keys or a chunk of them. A tile's rows are (token,
 // query head) pairs of one key head's group, token by token, so that every key
 // tile is read once for the whole group; a tile of 128 rows holds 128/G tokens.
-// The kernel is persistent: a CTA per SM takes items in turn, and each role
-// walks the same list on its own, so the loads and the first score product of
-// an item run under the softmax and the output of the one before.
+// The kernel is persistent: a CTA per SM takes items in turn, and the loads and
+// the first score product of an item run under the softmax and the output of
+// the one before.
 //   warps 0-7   softmax, one thread a row (warpgroup t owns tile t and TMEM
 //               lanes 0..127): online softmax in the log2 domain, the running
 //               maximum m and sum l in fp32, the accumulator rescaled only when
@@ -16,10 +16,12 @@
 //               Warps w and w + 4 share an SM sub-partition and take turns on
 //               its exponential unit.
 //   warp 8      tcgen05.mma issuer: S_t = Q_t K^T, O_t += P_t V.
-//   warps 9, 11 where a value tile holds rows that must not count (behind the
-//               segment's end, or masked) they write zeros over them: P is 0
+//   warp 9      where a value tile holds rows that must not count (behind the
+//               segment's end, or masked) it writes zeros over them: P is 0
 //               there, but 0 times a NaN or an infinity is not.
 //   warp 10     TMA producer.
+//   warp 11     finds the items (a search over the segments) ahead of the others
+//               and hands them over in a ring of four.
 // A key tile's products stop at its last key (in steps of 16). Items with no
 // more rows than one tile leave the second tile out.
 //
@@ -54,9 +56,24 @@ struct CrossParams {
     int32_t slot_rows;
 };
 
-constexpr int kCrossTable = 1024;       // entries of the segment table
+constexpr int kCrossTable = 256;        // entries of the segment table
 constexpr int kCrossItems = 296;        // items that a split aims at: two for each of 148 SMs
 constexpr int kCrossMinChunk = 2;       // key tiles of a chunk at least
+
+// An item in the ring (byte offsets).
+enum : int {
+    CX_Q0 = 0,         // first query token
+    CX_Q_LEFT = 4,     // query tokens of this item (at most two tiles)
+    CX_HEAD = 8,       // block of hp query heads
+    CX_K0 = 12,        // first key token
+    CX_K_LEFT = 16,    // keys from there to the segment's end
+    CX_N_KV = 20,      // key tiles; negative: no more items
+    CX_SPLITS = 24,    // chunks that these rows' keys are split into
+    CX_GROUP = 28,     // item number of the first of them
+    CX_ITEM = 32,      // item number
+    CX_BYTES = 48
+};
+constexpr int kCrossRing = 4;
 
 template <int D>
 struct CrossCfg {
@@ -64,9 +81,11 @@ struct CrossCfg {
     static constexpr int BOX_BYTES = 128 * 128;
     static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
     static constexpr int OFF_Q = 0, OFF_K = 2 * TILE_BYTES, OFF_V = 4 * TILE_BYTES;
-    static constexpr int OFF_BAR = 6 * TILE_BYTES;
-    static constexpr int OFF_TABLE = OFF_BAR + 512;
-    static constexpr int SMEM_BYTES = OFF_TABLE + (kCrossTable + 1) * 4 + 60 + 1024;
+    static constexpr int OFF_OUT = 6 * TILE_BYTES;            // 4 KB for each softmax warp
+    static constexpr int OFF_BAR = OFF_OUT + 8 * 4096;
+    static constexpr int OFF_PLAN = OFF_BAR + 512;
+    static constexpr int OFF_RING = OFF_PLAN + kCrossTable * 4 + 64;
+    static constexpr int SMEM_BYTES = OFF_RING + kCrossRing * CX_BYTES + 1024;   // + alignment slack
     static constexpr uint32_t COL_S = 0, COL_O = 256;   // S_t at 128 t, O_t at 256 + 128 t
     static constexpr int THREADS = 384;
     // 168 registers a thread at launch; the producer warpgroup drops to 56 and
@@ -77,23 +96,15 @@ struct CrossCfg {
 enum : int {
     CB_QFULL = 0, CB_QEMPTY = 2, CB_KFULL = 4, CB_KEMPTY = 6, CB_VFULL = 8, CB_VEMPTY = 10,
     CB_VFIX = 12, CB_SFULL = 14, CB_P1 = 16, CB_P2 = 18, CB_OFULL = 20, CB_DRAIN = 22,
-    CB_TURN = 23, CB_COUNT = 31
+    CB_TURN = 24,   // CB_TURN * 8 is a multiple of 64
+    CB_IFULL = 32, CB_IEMPTY = 36, CB_JOIN = 40, CB_COUNT = 42
 };
 
-struct CrossItem {
-    int q0, q_left;      // first query token, tokens in this item (at most two tiles)
-    int head;            // block of hp query heads
-    int k0, k_left;      // first key token, keys from there to the segment's end
-    int n_kv;            // key tiles
-    int splits, group;   // chunks of these rows, item number of the first
-};
-
-struct CrossPlan {
-    const int *table;    // items before entry i, without the head blocks
-    int entries, stride; // segments an entry
-    int chunk;           // key tiles a chunk at most
-    int total;           // items
-};
+// The plan of a launch in shared memory, from one address on: the key tiles of a
+// chunk at most, the items in all, then the table: items (without the head blocks)
+// before entry i, an entry holding cross_stride(nseg) segments.
+enum : int { CP_CHUNK = 0, CP_TOTAL = 4, CP_TABLE = 8 };
+__device__ __forceinline__ int cross_stride(int nseg) { return (nseg + kCrossTable - 1) / kCrossTable; }
 
 __device__ __forceinline__ void cross_segment(const CrossParams &p, int chunk, int s, int &blocks,
                                               int &tiles, int &splits) {
@@ -103,32 +114,38 @@ __device__ __forceinline__ void cross_segment(const CrossParams &p, int chunk, i
     splits = tiles == 0 ? 1 : (tiles + chunk - 1) / chunk;
 }
 
-__device__ __forceinline__ CrossItem cross_item(const CrossParams &p, const CrossPlan &plan, int it) {
-    const int unit = it / p.heads_blocks;
-    int lo = 0, hi = plan.entries;   // the last entry that begins at or before unit
+// Writes item `it` to the ring slot `to`.
+__device__ __forceinline__ void cross_find_item(const CrossParams &p, uint32_t plan, int it,
+                                                uint32_t to) {
+    const int unit = it / p.heads_blocks, chunk = lds32(plan + CP_CHUNK);
+    const int stride = cross_stride(p.nseg);
+    int lo = 0, hi = (p.nseg + stride - 1) / stride;   // the last entry that begins at or before unit
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (plan.table[mid] <= unit) lo = mid; else hi = mid;
+        if (lds32(plan + CP_TABLE + mid * 4) <= unit) lo = mid; else hi = mid;
     }
-    int s = lo * plan.stride, before = plan.table[lo], blocks, tiles, splits;
+    int s = lo * stride, before = lds32(plan + CP_TABLE + lo * 4), blocks, tiles, splits;
     while (true) {
-        cross_segment(p, plan.chunk, s, blocks, tiles, splits);
+        cross_segment(p, chunk, s, blocks, tiles, splits);
         if (unit < before + blocks * splits || s + 1 >= p.nseg) break;
         before += blocks * splits;
         ++s;
     }
     const int in_seg = unit - before, block = in_seg / splits, split = in_seg - block * splits;
-    const int first = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
-    CrossItem x;
-    x.head = it - unit * p.heads_blocks;
-    x.q0 = p.cu_q[s] + block * 2 * p.tokens;
-    x.q_left = min(p.cu_q[s + 1] - x.q0, 2 * p.tokens);
-    x.k0 = p.cu_k[s] + first * 128;
-    x.k_left = p.cu_k[s + 1] - x.k0;
-    x.n_kv = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits) - first;
-    x.splits = splits;
-    x.group = (before + block * splits) * p.heads_blocks + x.head;
-    return x;
+    // chunks of tiles / splits key tiles, the first ones of one more
+    const int each = tiles / splits, more = tiles - each * splits;
+    const int first = split * each + min(split, more);
+    const int head = it - unit * p.heads_blocks;
+    const int q0 = p.cu_q[s] + block * 2 * p.tokens, k0 = p.cu_k[s] + first * 128;
+    sts32(to + CX_Q0, q0);
+    sts32(to + CX_Q_LEFT, min(p.cu_q[s + 1] - q0, 2 * p.tokens));
+    sts32(to + CX_HEAD, head);
+    sts32(to + CX_K0, k0);
+    sts32(to + CX_K_LEFT, p.cu_k[s + 1] - k0);
+    sts32(to + CX_N_KV, each + (split < more));
+    sts32(to + CX_SPLITS, splits);
+    sts32(to + CX_GROUP, (before + block * splits) * p.heads_blocks + head);
+    sts32(to + CX_ITEM, it);
 }
 
 // 3-D tile of a [N, H, D] tensor's map (dims D, H, N).
@@ -136,6 +153,15 @@ __device__ __forceinline__ void cross_load(uint8_t *dst, const CUtensorMap *map,
                                            int boxes, int head, int token) {
     for (int b = 0; b < boxes; ++b)
         tma_load_3d(dst + b * 128 * 128, map, bar, b * 64, head, token);
+}
+
+// s = -infinity unless `keep`. In place: written as a select, the compiler kept two
+// copies of the score registers and spilled.
+__device__ __forceinline__ void drop_unless(uint32_t &s, uint32_t keep) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.u32 p, %1, 0;\n\t"
+        "@p mov.b32 %0, 0xff800000;\n\t}" : "+r"(s) : "r"(keep));
 }
 
 // 2^x for two lanes on the FMA and integer pipes: x = j + f with j = rint(x)
@@ -190,16 +216,13 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + CB_COUNT);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *last_s = abort + 1;                                     // [2]
-    unsigned long long *units_s = reinterpret_cast<unsigned long long *>(bars + CB_COUNT + 3);
-    int *table = reinterpret_cast<int *>(smem + C::OFF_TABLE);
+    unsigned long long *units_s = reinterpret_cast<unsigned long long *>(bars + CB_COUNT + 2);
+    int *table = reinterpret_cast<int *>(smem + C::OFF_PLAN + CP_TABLE);
+    const uint32_t plan = smem_u32(smem + C::OFF_PLAN);
 
     // ---- the boundaries, checked by every CTA; the work they make
-    CrossPlan plan;
-    plan.stride = (p.nseg + kCrossTable - 1) / kCrossTable;
-    plan.entries = (p.nseg + plan.stride - 1) / plan.stride;
-    plan.table = table;
-    plan.chunk = 1 << 24;   // more than any segment has: no split
+    const int stride = cross_stride(p.nseg), entries = (p.nseg + stride - 1) / stride;
+    int chunk = 1 << 24;   // more than any segment has: no split
     if (tid == 0) *units_s = 0;
     int bad = 0;
     unsigned long long units = 0;
@@ -222,14 +245,14 @@ __global__ void __launch_bounds__(384, 1)
         if (units) atomicAdd(units_s, units);
         __syncthreads();
         const unsigned long long all = *units_s * static_cast<unsigned>(p.heads_blocks);
-        plan.chunk = static_cast<int>(max((all + kCrossItems - 1) / kCrossItems,
-                                          static_cast<unsigned long long>(kCrossMinChunk)));
+        chunk = static_cast<int>(max((all + kCrossItems - 1) / kCrossItems,
+                                     static_cast<unsigned long long>(kCrossMinChunk)));
     }
-    for (int e = tid; e < plan.entries; e += C::THREADS) {
+    for (int e = tid; e < entries; e += C::THREADS) {
         int sum = 0;
-        for (int s = e * plan.stride; s < min((e + 1) * plan.stride, p.nseg); ++s) {
+        for (int s = e * stride; s < min((e + 1) * stride, p.nseg); ++s) {
             int blocks, tiles, splits;
-            cross_segment(p, plan.chunk, s, blocks, tiles, splits);
+            cross_segment(p, chunk, s, blocks, tiles, splits);
             sum += blocks * splits;
         }
         table[e + 1] = sum;
@@ -243,13 +266,18 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&bars[CB_KEMPTY + s], 2);   // one commit for each tile
             mbar_init(&bars[CB_VFULL + s], 1);
             mbar_init(&bars[CB_VEMPTY + s], 2);
-            mbar_init(&bars[CB_VFIX + s], 2);     // warps 9 and 11
+            mbar_init(&bars[CB_VFIX + s], 1);
             mbar_init(&bars[CB_SFULL + s], 1);
             mbar_init(&bars[CB_P1 + s], 4);
             mbar_init(&bars[CB_P2 + s], 4);
             mbar_init(&bars[CB_OFULL + s], 1);
+            mbar_init(&bars[CB_JOIN + s], 4);
         }
         mbar_init(&bars[CB_DRAIN], 1);
+        for (int i = 0; i < kCrossRing; ++i) {
+            mbar_init(&bars[CB_IFULL + i], 1);
+            mbar_init(&bars[CB_IEMPTY + i], 11);   // every warp but the one that fills it
+        }
         for (int i = 0; i < 8; ++i) mbar_init(&bars[CB_TURN + i], 1);
         *abort = 0;
         fence_mbar_init();
@@ -266,42 +294,79 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     if (warp == 0) {   // running sums of the table
         int carry = 0;
-        for (int e = 0; e < plan.entries; e += 32) {
-            int x = e + lane < plan.entries ? table[e + lane + 1] : 0;
+        for (int e = 0; e < entries; e += 32) {
+            int x = e + lane < entries ? table[e + lane + 1] : 0;
             for (int d = 1; d < 32; d *= 2) {
                 const int y = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += y;
             }
             x += carry;
-            if (e + lane < plan.entries) table[e + lane + 1] = x;
+            if (e + lane < entries) table[e + lane + 1] = x;
             carry = __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            sts32(plan + CP_CHUNK, chunk);
+            sts32(plan + CP_TOTAL, carry * p.heads_blocks);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    plan.total = table[plan.entries] * p.heads_blocks;
 
-    // keys of a key tile, and its MMA steps of 16 keys
-    auto keys_in = [](const CrossItem &x, int j) { return min(x.k_left - j * 128, 128); };
+    const uint32_t bar0 = smem_u32(smem) + C::OFF_BAR, abort_at = bar0 + CB_COUNT * 8 + 4;
+    const uint32_t last_at = abort_at + 4;   // [2]
+    const uint32_t ring = smem_u32(smem) + C::OFF_RING;
+    auto wait = [&](int bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_at(bar0 + bar * 8, parity, abort_at));
+    };
+    // The n-th item: its ring slot, when it is there, and its release by this warp.
+    auto item_wait = [&](uint32_t n) {
+        return wait(CB_IFULL + n % kCrossRing, (n / kCrossRing) & 1);
+    };
+    auto item_done = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(bar0 + (CB_IEMPTY + n % kCrossRing) * 8);
+    };
+    // keys of key tile j
+    auto keys_in = [](int k_left, int j) { return min(k_left - j * 128, 128); };
 
-    if (warp == 10) {
+    if (warp == 11) {
+        // ============================ items ===================================
+        reg_dealloc<C::REGS_PRODUCER>();
+        uint32_t n = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; ok; it += gridDim.x, ++n) {
+            const bool more = it < lds32(plan + CP_TOTAL);
+            ok = wait(CB_IEMPTY + n % kCrossRing, ((n / kCrossRing) & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t to = ring + (n % kCrossRing) * CX_BYTES;
+                if (more) cross_find_item(p, plan, it, to);
+                else sts32(to + CX_N_KV, -1);
+                mbar_arrive_at(bar0 + (CB_IFULL + n % kCrossRing) * 8);
+            }
+            if (!more) break;
+        }
+        if (!ok && lane == 0) give_up(abort, p.status);
+        __syncwarp();
+    } else if (warp == 10) {
         // ============================ TMA producer ============================
         reg_dealloc<C::REGS_PRODUCER>();
         const uint32_t leader = elect_one();
         const uint32_t q_bytes = static_cast<uint32_t>(C::NBOX * 128 * p.hp * p.tokens);
-        auto wait = [&](int bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort));
-        };
         int nq[2] = {0, 0}, nk = 0, nv = 0;   // loads issued
         bool ok = true;
-        for (int it = blockIdx.x; ok && it < plan.total; it += gridDim.x) {
-            const CrossItem x = cross_item(p, plan, it);
-            if (x.n_kv == 0) continue;
-            const int kv_head = x.head * p.hp / (p.Hq / p.Hk);
-            const int n_t = x.q_left > p.tokens ? 2 : 1;
-            for (int j = 0; ok && j < x.n_kv; ++j) {
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            if (!ok) break;
+            const uint32_t x = ring + (n % kCrossRing) * CX_BYTES;
+            const int n_kv = lds32(x + CX_N_KV), head = lds32(x + CX_HEAD) * p.hp;
+            const int kv_head = head / (p.Hq / p.Hk), q0 = lds32(x + CX_Q0), k0 = lds32(x + CX_K0);
+            const int n_t = lds32(x + CX_Q_LEFT) > p.tokens ? 2 : 1;
+            item_done(n);
+            if (n_kv < 0) break;
+            for (int j = 0; ok && j < n_kv; ++j) {
                 if (j == 0)
                     for (int t = 0; ok && t < n_t; ++t) {
                         ok = wait(CB_QEMPTY + t, (nq[t] & 1) ^ 1);
@@ -309,8 +374,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (leader) {
                             mbar_arrive_expect_tx(&bars[CB_QFULL + t], q_bytes);
                             cross_load(smem + C::OFF_Q + t * C::TILE_BYTES, &tmQ,
-                                       &bars[CB_QFULL + t], C::NBOX, x.head * p.hp,
-                                       x.q0 + t * p.tokens);
+                                       &bars[CB_QFULL + t], C::NBOX, head, q0 + t * p.tokens);
                         }
                         ++nq[t];
                     }
@@ -321,7 +385,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (leader) {
                     mbar_arrive_expect_tx(&bars[CB_KFULL + s], C::TILE_BYTES);
                     cross_load(smem + C::OFF_K + s * C::TILE_BYTES, &tmK, &bars[CB_KFULL + s],
-                               C::NBOX, kv_head, x.k0 + j * 128);
+                               C::NBOX, kv_head, k0 + j * 128);
                 }
                 ++nk;
                 ok = wait(CB_VEMPTY + s, ((nv >> 1) & 1) ^ 1);
@@ -329,7 +393,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (leader) {
                     mbar_arrive_expect_tx(&bars[CB_VFULL + s], C::TILE_BYTES);
                     cross_load(smem + C::OFF_V + s * C::TILE_BYTES, &tmV, &bars[CB_VFULL + s],
-                               C::NBOX, kv_head, x.k0 + j * 128);
+                               C::NBOX, kv_head, k0 + j * 128);
                 }
                 ++nv;
             }
@@ -345,38 +409,42 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_wait(&bars[CB_VFULL + (j & 1)], (j >> 1) & 1, nullptr);
         }
         __syncwarp();
-    } else if (warp == 9 || warp == 11) {
+    } else if (warp == 9) {
         // ============================ value rows that must not count ==========
         reg_dealloc<C::REGS_PRODUCER>();
-        const int half = warp == 11;
         int nv = 0;
         bool ok = true;
-        for (int it = blockIdx.x; ok && it < plan.total; it += gridDim.x) {
-            const CrossItem x = cross_item(p, plan, it);
-            for (int j = 0; ok && j < x.n_kv; ++j, ++nv) {
-                const int keys = keys_in(x, j), s = nv & 1, rows = (keys + 15) / 16 * 16;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            if (!ok) break;
+            const uint32_t x = ring + (n % kCrossRing) * CX_BYTES;
+            const int n_kv = lds32(x + CX_N_KV), k0 = lds32(x + CX_K0), k_left = lds32(x + CX_K_LEFT);
+            item_done(n);
+            if (n_kv < 0) break;
+            for (int j = 0; ok && j < n_kv; ++j, ++nv) {
+                const int keys = keys_in(k_left, j), s = nv & 1, rows = (keys + 15) / 16 * 16;
                 // every phase is waited for, those of tiles that need nothing too: a
                 // parity tells a phase from its neighbours only
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars[CB_VFULL + s], (nv >> 1) & 1, abort));
+                ok = wait(CB_VFULL + s, (nv >> 1) & 1);
                 if (!ok) break;
                 if (p.mask == nullptr && keys % 16 == 0) continue;
                 uint8_t *v = smem + C::OFF_V + s * C::TILE_BYTES;
-                // four rows a step, eight lanes a row; warp 9 the even fours
-                for (int r0 = half * 4; r0 < rows; r0 += 8) {
+                // four rows a step, eight lanes a row; without a mask the last step of 16 only
+                for (int r0 = p.mask == nullptr ? rows - 16 : 0; r0 < rows; r0 += 4) {
                     const int r = r0 + lane / 8;
-                    const bool counts = r < keys &&
-                        (p.mask == nullptr || p.mask[x.k0 + j * 128 + r] != 0);
-                    if (!counts && r < rows)
+                    const bool counts = r < keys && (p.mask == nullptr || p.mask[k0 + j * 128 + r] != 0);
+                    if (!counts)
                         for (int b = 0; b < C::NBOX; ++b)
                             *reinterpret_cast<uint4 *>(v + b * C::BOX_BYTES + r * 128 +
                                                        (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[CB_VFIX + s]);
+                if (lane == 0) mbar_arrive_at(bar0 + (CB_VFIX + s) * 8);
             }
         }
         if (!ok && lane == 0) give_up(abort, p.status);
+        __syncwarp();
     } else if (warp == 8) {
         // ============================ MMA issuer ==============================
         reg_dealloc<C::REGS_PRODUCER>();
@@ -386,8 +454,8 @@ __global__ void __launch_bounds__(384, 1)
         const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
         const uint64_t dK = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
         const uint64_t dV = sdesc_sw128(smem_u32(smem + C::OFF_V), C::BOX_BYTES, 1024);
-        auto wait = [&](int bar, uint32_t parity) {
-            const bool r = __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort));
+        auto mma_wait = [&](int bar, uint32_t parity) {
+            const bool r = wait(bar, parity);
             tc_fence_after();
             return r;
         };
@@ -413,42 +481,46 @@ __global__ void __launch_bounds__(384, 1)
         int nkv = 0;                         // key tiles so far
         uint32_t fixes = 0;                  // parity of the next VFIX phase, a bit a stage
         bool ok = true;
-        for (int it = blockIdx.x; ok && it < plan.total; it += gridDim.x) {
-            const CrossItem x = cross_item(p, plan, it);
-            if (x.n_kv == 0) continue;
-            const int n_t = x.q_left > p.tokens ? 2 : 1;
-            for (int t = 0; ok && t < n_t; ++t) {
-                ok = wait(CB_QFULL + t, nq[t] & 1) && wait(CB_KFULL + (nkv & 1), (nkv >> 1) & 1);
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            if (!ok) break;
+            const uint32_t x = ring + (n % kCrossRing) * CX_BYTES;
+            const int n_kv = lds32(x + CX_N_KV), k_left = lds32(x + CX_K_LEFT);
+            const int n_t = lds32(x + CX_Q_LEFT) > p.tokens ? 2 : 1;
+            item_done(n);
+            if (n_kv < 0) break;
+            for (int t = 0; ok && n_kv > 0 && t < n_t; ++t) {
+                ok = mma_wait(CB_QFULL + t, nq[t] & 1) && mma_wait(CB_KFULL + (nkv & 1), (nkv >> 1) & 1);
                 if (!ok) break;
-                issue_s(t, nkv & 1, keys_in(x, 0));
+                issue_s(t, nkv & 1, keys_in(k_left, 0));
                 umma_commit_w(&bars[CB_SFULL + t], leader);
                 umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
                 if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
-                if (x.n_kv == 1) umma_commit_w(&bars[CB_QEMPTY + t], leader);
+                if (n_kv == 1) umma_commit_w(&bars[CB_QEMPTY + t], leader);
                 ++nq[t];
             }
-            for (int j = 0; ok && j < x.n_kv; ++j, ++nkv) {
-                const int s = nkv & 1, keys = keys_in(x, j), n16 = (keys + 15) / 16;
-                const bool more = j + 1 < x.n_kv, fix = p.mask != nullptr || keys % 16 != 0;
+            for (int j = 0; ok && j < n_kv; ++j, ++nkv) {
+                const int s = nkv & 1, keys = keys_in(k_left, j), n16 = (keys + 15) / 16;
+                const bool more = j + 1 < n_kv, fix = p.mask != nullptr || keys % 16 != 0;
                 for (int t = 0; ok && t < n_t; ++t) {
-                    ok = wait(CB_P1 + t, g[t] & 1) && wait(CB_VFULL + s, (nkv >> 1) & 1);
-                    if (ok && fix && t == 0) ok = wait(CB_VFIX + s, (fixes >> s) & 1);
+                    ok = mma_wait(CB_P1 + t, g[t] & 1) && mma_wait(CB_VFULL + s, (nkv >> 1) & 1);
+                    if (ok && fix && t == 0) ok = mma_wait(CB_VFIX + s, (fixes >> s) & 1);
                     if (!ok) break;
                     issue_pv(t, s, 0, min(n16, 4), j > 0);
-                    ok = wait(CB_P2 + t, g[t] & 1);
+                    ok = mma_wait(CB_P2 + t, g[t] & 1);
                     if (!ok) break;
                     issue_pv(t, s, 4, n16, true);
                     umma_commit_w(&bars[CB_VEMPTY + s], leader);
                     if (n_t == 1) umma_commit_w(&bars[CB_VEMPTY + s], leader);
                     if (more) {
                         const int s1 = (nkv + 1) & 1;
-                        ok = wait(CB_KFULL + s1, ((nkv + 1) >> 1) & 1);
+                        ok = mma_wait(CB_KFULL + s1, ((nkv + 1) >> 1) & 1);
                         if (!ok) break;
-                        issue_s(t, s1, keys_in(x, j + 1));
+                        issue_s(t, s1, keys_in(k_left, j + 1));
                         umma_commit_w(&bars[CB_SFULL + t], leader);
                         umma_commit_w(&bars[CB_KEMPTY + s1], leader);
                         if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + s1], leader);
-                        if (j + 2 == x.n_kv) umma_commit_w(&bars[CB_QEMPTY + t], leader);
+                        if (j + 2 == n_kv) umma_commit_w(&bars[CB_QEMPTY + t], leader);
                     } else {
                         umma_commit_w(&bars[CB_OFULL + t], leader);
                     }
@@ -470,42 +542,76 @@ __global__ void __launch_bounds__(384, 1)
         const int r = tid & 127;                 // row of the tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + C::COL_S + t * 128;
-        const uint32_t tO = tmem + lane_off + C::COL_O + t * 128;
+        const uint32_t tO = tS + (C::COL_O - C::COL_S);
         const float sl2 = p.scale_log2;
-        auto wait = [&](int bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort));
+        uint32_t par = 0;   // parities of the next phases: 1 S, 2 O, 4 turn, 8 join
+        // Barrier addresses from few registers: those of tile t, and this sub-partition's
+        // turns. Tile 0 waits for tile 1's last key tile in turn, tile 1 for tile 0's same
+        // one; each gives on the other's barrier, 32 bytes (of 64) away.
+        const uint32_t bar_t = bar0 + t * 8;
+        const uint32_t turn = bar0 + (CB_TURN + 4 * t + (warp & 3)) * 8;
+        auto wait_t = [&](int bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_at(bar_t + bar * 8, parity, abort_at));
         };
-        int items = 0, g = 0, turns = 0;   // of this tile: items, key tiles, key tiles in turn
-        // after a wait that gave up, the warps go on to meet at named_sync
-        bool ok = true;
-        for (int it = blockIdx.x; it < plan.total; it += gridDim.x) {
-            const CrossItem x = cross_item(p, plan, it);
-            const bool two = x.q_left > p.tokens;
+        // (tile 0's first wait is for the phase before the first, which counts as over)
+        auto take_turn = [&]() {
+            const bool r = __all_sync(0xffffffffu,
+                                      mbar_wait_at(turn, ((par >> 2) & 1) ^ (t == 0), abort_at));
+            par ^= 4u;
+            return r;
+        };
+        auto give_turn = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(turn ^ 32u);
+        };
+        bool ok = true;   // false from the first wait that gave up
+        for (uint32_t n = 0; ; item_done(n), ++n) {
+            if (!ok || !item_wait(n)) {
+                if (lane == 0) give_up(abort, p.status);
+                break;
+            }
+            const uint32_t xs = ring + (n % kCrossRing) * CX_BYTES;   // read again after the loop
+            const int n_kv = lds32(xs + CX_N_KV), k_left = lds32(xs + CX_K_LEFT);
+            if (n_kv < 0) break;
+            const bool two = lds32(xs + CX_Q_LEFT) > p.tokens;
             if (t == 1 && !two) continue;
-            const int rows = min(x.q_left - t * p.tokens, p.tokens) * p.hp;
-            const bool active = (warp & 3) * 32 < rows;   // a warp without rows only signals
-            const bool row_ok = r < rows;
-            const int tok = r / p.hp;
-            const int qrow = x.q0 + t * p.tokens + tok, head = x.head * p.hp + r - tok * p.hp;
+            // a warp without rows only signals
+            const bool active = (warp & 3) * 32 <
+                                min(lds32(xs + CX_Q_LEFT) - t * p.tokens, p.tokens) * p.hp;
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; ok && j < x.n_kv; ++j, ++g) {
-                const int keys = keys_in(x, j);
-                uint32_t valid[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                const bool part = keys < 128 || p.mask != nullptr;
-                if (part) {
+            for (int j = 0; ok && !active && j < n_kv; ++j) {
+                ok = wait_t(CB_SFULL, par & 1);
+                par ^= 1u;
+                if (ok && two) {
+                    ok = take_turn();
+                    give_turn();
+                }
+                if (lane == 0) {
+                    mbar_arrive_at(bar_t + CB_P1 * 8);
+                    mbar_arrive_at(bar_t + CB_P2 * 8);
+                }
+            }
+            // One key tile of this warp's rows, `keys` of them left; `part`: not all count.
+            // Two copies of the code, so that only one of them pays for the masking.
+            auto softmax_tile = [&](auto part, int keys, int j) {
+                uint32_t s[128];
+#pragma unroll
+                for (int i = 0; i < 128; i += 16)
+                    tmem_ld16(tS + i, *reinterpret_cast<uint32_t(*)[16]>(&s[i]));
+                tmem_wait_ld();
+                if constexpr (decltype(part)::value) {
+                    uint32_t any = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int c = i * 32 + lane;
-                        valid[i] = __ballot_sync(0xffffffffu, c < keys &&
-                            (p.mask == nullptr || p.mask[x.k0 + j * 128 + c] != 0));
+                        const uint32_t valid = __ballot_sync(0xffffffffu, c < keys &&
+                            (p.mask == nullptr || p.mask[lds32(xs + CX_K0) + j * 128 + c] != 0));
+                        any |= valid;
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            drop_unless(s[i * 32 + q], valid & (1u << q));
                     }
-                }
-                ok = wait(CB_SFULL + t, g & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const bool none = (valid[0] | valid[1] | valid[2] | valid[3]) == 0;
-                if (!active || none) {
-                    if (active) {
+                    if (any == 0) {   // no key of this tile counts: P = 0, nothing else changes
                         uint32_t z[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -513,54 +619,26 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_st32(tS + 32, z);
                         tmem_wait_st();
                         tc_fence_before();
+                        if (two) {
+                            ok = take_turn();
+                            give_turn();
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive_at(bar_t + CB_P1 * 8);
+                            mbar_arrive_at(bar_t + CB_P2 * 8);
+                        }
+                        return;
                     }
-                    __syncwarp();
-                    if (two) {
-                        if (t == 1 || turns > 0)
-                            ok = wait(t == 0 ? CB_TURN + (warp & 3) : CB_TURN + 4 + (warp & 3),
-                                      static_cast<uint32_t>(t == 0 ? (turns - 1) & 1 : turns & 1));
-                        if (!ok) break;
-                        ++turns;
-                        if (lane == 0)
-                            mbar_arrive(&bars[t == 0 ? CB_TURN + 4 + (warp & 3) : CB_TURN + (warp & 3)]);
-                    }
-                    if (lane == 0) {
-                        mbar_arrive(&bars[CB_P1 + t]);
-                        mbar_arrive(&bars[CB_P2 + t]);
-                    }
-                    continue;
-                }
-                const bool long_tile = keys > 64;
-                uint32_t s[128];
-                tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                if (long_tile) {
-                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
-                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
-                }
-                tmem_wait_ld();
-                if (part) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (!((valid[c >> 5] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
                 }
                 float mq[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mq[i] = __uint_as_float(s[i]);
 #pragma unroll
-                for (int c = 8; c < 56; c += 16)
+                for (int c = 8; c < 128; c += 16)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         mq[i] = fmax3(mq[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mq[i] = fmaxf(mq[i], __uint_as_float(s[56 + i]));
-                if (long_tile) {
-#pragma unroll
-                    for (int c = 64; c < 128; c += 16)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            mq[i] = fmax3(mq[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
-                }
                 const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
                                        fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
                 const float m_new = mx * sl2;
@@ -592,10 +670,9 @@ __global__ void __launch_bounds__(384, 1)
                         pk[c] = pack2<T>(p0, p1);
                     }
                 };
-                if (two && (t == 1 || turns > 0)) {
-                    ok = wait(t == 0 ? CB_TURN + (warp & 3) : CB_TURN + 4 + (warp & 3),
-                              static_cast<uint32_t>(t == 0 ? (turns - 1) & 1 : turns & 1));
-                    if (!ok) break;
+                if (two) {
+                    ok = take_turn();
+                    if (!ok) return;
                 }
                 exp_half(0);
                 tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
@@ -614,48 +691,69 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[CB_P1 + t]);
-                if (long_tile) exp_half(1);
-                if (two) {
-                    ++turns;
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&bars[t == 0 ? CB_TURN + 4 + (warp & 3) : CB_TURN + (warp & 3)]);
-                }
+                if (lane == 0) mbar_arrive_at(bar_t + CB_P1 * 8);
+                exp_half(1);
+                if (two) give_turn();
                 l += f2_sum(acc0) + f2_sum(acc1);
-                if (long_tile) {
-                    tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-                    tmem_wait_st();
-                    tc_fence_before();
-                }
+                tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                tmem_wait_st();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[CB_P2 + t]);
+                if (lane == 0) mbar_arrive_at(bar_t + CB_P2 * 8);
+            };
+            for (int j = 0; ok && active && j < n_kv; ++j) {
+                const int keys = k_left - j * 128;   // and more, behind the tile
+                ok = wait_t(CB_SFULL, par & 1);
+                par ^= 1u;
+                if (!ok) break;
+                tc_fence_after();
+                if (keys < 128 || p.mask != nullptr) softmax_tile(std::true_type{}, keys, j);
+                else softmax_tile(std::false_type{}, keys, j);
             }
-            if (x.n_kv > 0) {
-                ok = ok && wait(CB_OFULL + t, items & 1);
-                ++items;
+            if (n_kv > 0) {
+                ok = ok && wait_t(CB_OFULL, (par >> 1) & 1);
+                par ^= 2u;
                 tc_fence_after();
             }
             if (!ok && lane == 0) give_up(abort, p.status);
-            if (x.splits == 1) {
+            const int rows = min(lds32(xs + CX_Q_LEFT) - t * p.tokens, p.tokens) * p.hp;
+            const bool row_ok = r < rows;
+            const int tok = r / p.hp, splits = lds32(xs + CX_SPLITS);
+            const int qrow = lds32(xs + CX_Q0) + t * p.tokens + tok, head = lds32(xs + CX_HEAD) * p.hp + r - tok * p.hp;
+            if (splits == 1) {
                 if (!ok || !active) continue;
                 const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
-                uint4 *orow = reinterpret_cast<uint4 *>(
-                    static_cast<T *>(p.o) + qrow * p.ldo + static_cast<int64_t>(head) * D);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    if (x.n_kv > 0) tmem_ld32(tO + c * 32, o);
+                // 64 channels at a time through shared memory (16-byte pieces, their
+                // place exclusive-or'ed with the row), so that a store writes four
+                // whole 128-byte lines; 16 bytes of 32 rows at a time cost 4 to 5
+                // thousand cycles a tile (8 now, 1 for D = 64) and half-written sectors
+                const int64_t at = row_ok ? qrow * p.ldo + static_cast<int64_t>(head) * D : -1;
+                const uint32_t out = smem_u32(smem) + C::OFF_OUT + warp * 4096;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 64) {
+                    uint32_t o[64];
+                    if (n_kv > 0) {
+                        tmem_ld32(tO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+                        tmem_ld32(tO + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                    }
                     tmem_wait_ld();
-                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = l > 0.0f ? pack2<T>(__uint_as_float(o[2 * i]) * inv_l,
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = l > 0.0f ? pack2<T>(__uint_as_float(o[2 * i]) * inv_l,
                                                    __uint_as_float(o[2 * i + 1]) * inv_l) : 0u;
-                    if (row_ok) {
+                    __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            orow[c * 4 + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i)
+                        sts128(out + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1],
+                               o[4 * i + 2], o[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + lane / 8, piece = lane & 7;
+                        const int64_t row_at = __shfl_sync(0xffffffffu, at, rr);
+                        const uint4 v = lds128(out + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                        if (row_at >= 0)
+                            *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + row_at + c + piece * 8) = v;
                     }
                 }
                 if (row_ok && p.lse != nullptr)
@@ -667,7 +765,7 @@ __global__ void __launch_bounds__(384, 1)
             const int64_t slot = static_cast<int64_t>(p.slot_rows) * (D + 2);
             const int row0 = t * p.tokens * p.hp;     // of this tile in the slot
             if (ok && active) {
-                float *mine = p.parts + it * slot + static_cast<int64_t>(row0 + r) * (D + 2);
+                float *mine = p.parts + lds32(xs + CX_ITEM) * slot + static_cast<int64_t>(row0 + r) * (D + 2);
                 if (row_ok) *reinterpret_cast<float2 *>(mine) = make_float2(m, l);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -682,23 +780,33 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             __threadfence();
-            // the two tiles of an item may be at different items: a count and a flag each
-            named_sync(1 + t, 128);
+            // the two tiles may be at different items: a count, a flag and a barrier each
+            auto meet = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(bar_t + CB_JOIN * 8);
+                ok = wait_t(CB_JOIN, (par >> 3) & 1) && ok;
+                par ^= 8u;
+            };
+            meet();
             if (r == 0)
-                last_s[t] = *abort == 0 &&
-                            atomicAdd(&p.arrived[2 * x.group + t], 1) == x.splits - 1;
-            named_sync(1 + t, 128);
-            if (!last_s[t]) continue;
+                sts32(last_at + 4 * t, ok && lds32(abort_at) == 0 &&
+                      atomicAdd(&p.arrived[2 * lds32(xs + CX_GROUP) + t], 1) == splits - 1);
+            meet();
+            if (!ok) {
+                if (lane == 0) give_up(abort, p.status);
+                continue;
+            }
+            if (!lds32(last_at + 4 * t)) continue;
             __threadfence();
             for (int rr = warp & 3; rr < rows; rr += 4) {   // a warp a row
-                const float *all = p.parts + x.group * slot + static_cast<int64_t>(row0 + rr) * (D + 2);
+                const float *all = p.parts + lds32(xs + CX_GROUP) * slot + static_cast<int64_t>(row0 + rr) * (D + 2);
                 const int64_t step = slot * p.heads_blocks;
                 float mm = -INFINITY;
-                for (int i = 0; i < x.splits; ++i) mm = fmaxf(mm, __ldcg(all + i * step));
+                for (int i = 0; i < splits; ++i) mm = fmaxf(mm, __ldcg(all + i * step));
                 float sum = 0.0f, o[D / 32];
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
-                for (int i = 0; i < x.splits; ++i) {
+                for (int i = 0; i < splits; ++i) {
                     const float mi = __ldcg(all + i * step);
                     const float wgt = mi == -INFINITY ? 0.0f : ex2_approx(mi - mm);
                     sum = fmaf(wgt, __ldcg(all + i * step + 1), sum);
@@ -711,7 +819,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 const int rt = rr / p.hp;
-                const int row = x.q0 + t * p.tokens + rt, hh = x.head * p.hp + rr - rt * p.hp;
+                const int row = lds32(xs + CX_Q0) + t * p.tokens + rt, hh = lds32(xs + CX_HEAD) * p.hp + rr - rt * p.hp;
                 const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
                 T *orow = static_cast<T *>(p.o) + row * p.ldo + static_cast<int64_t>(hh) * D;
 #pragma unroll

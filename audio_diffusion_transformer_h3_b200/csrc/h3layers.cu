@@ -25,8 +25,46 @@ using h3host::kStatusBytes;
 
 struct Device {
     bool ready = false, sm100 = false;
+    bool cross_regs_ok = false;   // see set_up_kernels
     int sms = 0;
 };
+// Shared memory of the kernels that need more than the default, on the current
+// device. *cross_regs_ok: the launch allocation of every cross attention kernel
+// covers what its softmax warpgroups raise themselves to (the raise waits for
+// registers that the block holds from launch, so it would wait forever else).
+template <typename Kernel>
+cudaError_t big_smem(Kernel kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename T, int D>
+cudaError_t set_up_cross(bool *regs_ok) {
+    using C = h3::CrossCfg<D>;
+    cudaFuncAttributes a{};
+    cudaError_t e = big_smem(h3::cross_attn_kernel<T, D>, C::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, h3::cross_attn_kernel<T, D>);
+    if (a.numRegs * C::THREADS < 2 * 128 * C::REGS_SOFTMAX + 128 * C::REGS_PRODUCER) *regs_ok = false;
+    return e;
+}
+
+template <typename T>
+cudaError_t set_up_typed(bool *regs_ok) {
+    cudaError_t e;
+    if ((e = big_smem(h3::linear_tile_kernel<T, false>, h3::LinearTile::SMEM_BYTES)) != cudaSuccess ||
+        (e = big_smem(h3::linear_tile_kernel<T, true>, h3::LinearTile::SMEM_BYTES)) != cudaSuccess ||
+        (e = big_smem(h3::linear_skinny_kernel<T, false>, h3::LinearSkinny::SMEM_BYTES)) != cudaSuccess ||
+        (e = big_smem(h3::linear_skinny_kernel<T, true>, h3::LinearSkinny::SMEM_BYTES)) != cudaSuccess ||
+        (e = set_up_cross<T, 64>(regs_ok)) != cudaSuccess)
+        return e;
+    return set_up_cross<T, 128>(regs_ok);
+}
+
+cudaError_t set_up_kernels(bool *cross_regs_ok) {
+    *cross_regs_ok = true;
+    const cudaError_t e = set_up_typed<__nv_bfloat16>(cross_regs_ok);
+    return e != cudaSuccess ? e : set_up_typed<__half>(cross_regs_ok);
+}
+
 constexpr int kMaxDevices = 64;
 Device g_dev[kMaxDevices];
 std::mutex g_dev_mu;
@@ -45,6 +83,7 @@ h3_status device_info(const Device **out) {
             (e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
             return cuda_fail(e);
         d.sm100 = (major == 10 && minor == 0);
+        if (d.sm100 && (e = set_up_kernels(&d.cross_regs_ok)) != cudaSuccess) return cuda_fail(e);
         d.ready = true;
     }
     if (!d.sm100) return H3_ERR_UNSUPPORTED;
@@ -111,10 +150,34 @@ uint64_t phase_of(double f) {
     return scaled >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(scaled);
 }
 
+// Blocks of 256 places; the heads of few tokens are split so that the SMs have
+// two blocks each (a block computes its angles anew, so no further).
+template <typename T, bool Wide>
+void launch_rope_qk(h3::RopeQkParams &p, bool half, int sms, cudaStream_t st) {
+    constexpr int E = h3::RopeVec<T, Wide>::E;
+    const int pairs = half || !Wide ? E : E / 2;
+    const int places = p.rot / 2 / pairs + (p.copy ? (p.D - p.rot) / E : 0);
+    const int64_t blocks = (p.N * places + 255) / 256;
+    const int heads = p.Hq + p.Hk;
+    const int64_t parts = std::min<int64_t>(std::max<int64_t>(1, 2 * sms / blocks), (heads + 3) / 4);
+    p.head_chunk = static_cast<int32_t>((heads + parts - 1) / parts + 3) / 4 * 4;
+    const dim3 grid(static_cast<unsigned>(blocks),
+                    static_cast<unsigned>((heads + p.head_chunk - 1) / p.head_chunk));
+    if (half) h3::rope_qk_kernel<T, Wide, true><<<grid, 256, 0, st>>>(p);
+    else h3::rope_qk_kernel<T, Wide, false><<<grid, 256, 0, st>>>(p);
+}
+
+// 16-byte vectors where every row, head and (for the half layout) half of the
+// rotated part begins on one.
 template <typename T>
-void launch_rope_qk(const h3::RopeQkParams &p, int sms, cudaStream_t st) {
-    const int64_t cap = static_cast<int64_t>(sms) * 8;
-    h3::rope_qk_kernel<T><<<static_cast<int>(std::min(p.N, cap)), 256, 0, st>>>(p);
+void launch_rope_qk(h3::RopeQkParams &p, bool half, int sms, cudaStream_t st) {
+    constexpr int E = 16 / sizeof(T);
+    bool wide = p.D % E == 0 && (half ? p.rot / 2 : p.rot) % E == 0 && p.ldq % E == 0 &&
+                p.ldqo % E == 0 && aligned(p.q, 16) && aligned(p.qo, 16);
+    if (p.Hk > 0)
+        wide = wide && p.ldk % E == 0 && p.ldko % E == 0 && aligned(p.k, 16) && aligned(p.ko, 16);
+    if (wide) launch_rope_qk<T, true>(p, half, sms, st);
+    else launch_rope_qk<T, false>(p, half, sms, st);
 }
 
 // --------------------------------------------------------------------- linear
@@ -183,8 +246,6 @@ h3_status make_rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_
 template <typename Kernel>
 h3_status launch_mma(Kernel kernel, int grid, int threads, int smem, const CUtensorMap &a,
                      const CUtensorMap &b, const h3::LinearParams &p, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return cuda_fail(e);
     kernel<<<grid, threads, smem, st>>>(a, b, p);
     return launched();
 }
@@ -270,17 +331,7 @@ template <typename T, int D>
 h3_status launch_cross(const h3::CrossParams &p, int grid, const CUtensorMap &tq,
                        const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
     using C = h3::CrossCfg<D>;
-    const auto kernel = h3::cross_attn_kernel<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::SMEM_BYTES);
-    // the softmax warpgroups' raise waits for registers that the block holds
-    // from launch: a build whose launch allocation does not cover it is refused
-    cudaFuncAttributes a{};
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (a.numRegs * C::THREADS < 2 * 128 * C::REGS_SOFTMAX + 128 * C::REGS_PRODUCER)
-        return H3_ERR_UNSUPPORTED;
-    kernel<<<grid, C::THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
+    h3::cross_attn_kernel<T, D><<<grid, C::THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
     return launched();
 }
 
@@ -308,6 +359,7 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
         return H3_ERR_INVALID_ARG;
     const int64_t widest = std::max(std::max(ldq, ldq_out), Hk > 0 ? std::max(ldk, ldk_out) : 0);
     if (N > 0 && widest >= (int64_t{1} << 47) / N) return H3_ERR_INVALID_ARG;
+    if (N > (int64_t{1} << 30)) return H3_ERR_INVALID_ARG;   // blocks of a grid
     if (N > 0 && (q == nullptr || q_out == nullptr || positions == nullptr ||
                   (Hk > 0 && (k == nullptr || k_out == nullptr))))
         return H3_ERR_INVALID_ARG;
@@ -327,14 +379,16 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
     p.positions = positions;
     p.N = N;
     p.Hq = Hq; p.Hk = Hk; p.D = D; p.rot = cfg->rot_dim;
-    p.half = cfg->layout == H3_ROPE_HALF;
+    const bool half = cfg->layout == H3_ROPE_HALF;
+    // channels behind the rotated part are in place already where q and k are
+    p.copy = q != q_out || (Hk > 0 && k != k_out);
     p.attn_factor = static_cast<float>(cfg->attn_factor);
     for (int j = 0; j < h3::kRopeQkMaxPairs; ++j)
         p.phase[j] = j < cfg->rot_dim / 2 ? phase_of(f[j]) : 0;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == H3_BF16) launch_rope_qk<__nv_bfloat16>(p, d->sms, cs);
-    else if (dtype == H3_FP16) launch_rope_qk<__half>(p, d->sms, cs);
-    else launch_rope_qk<float>(p, d->sms, cs);
+    if (dtype == H3_BF16) launch_rope_qk<__nv_bfloat16>(p, half, d->sms, cs);
+    else if (dtype == H3_FP16) launch_rope_qk<__half>(p, half, d->sms, cs);
+    else launch_rope_qk<float>(p, half, d->sms, cs);
     return launched();
 }
 
@@ -456,6 +510,7 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     h3_status st = device_info(&d);
     if (st != H3_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (!d->cross_regs_ok) return H3_ERR_UNSUPPORTED;
     const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const cudaError_t e = cudaMemsetAsync(
