@@ -82,15 +82,12 @@ struct CrossCfg {
     static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
     static constexpr int OFF_Q = 0, OFF_K = 2 * TILE_BYTES, OFF_V = 4 * TILE_BYTES;
     static constexpr int OFF_OUT = 6 * TILE_BYTES;            // 4 KB for each softmax warp
-    static constexpr int OFF_BAR = OFF_OUT + 8 * 4096;
-    static constexpr int OFF_PLAN = OFF_BAR + 512;
-    static constexpr int OFF_RING = OFF_PLAN + kCrossTable * 4 + 64;
-    static constexpr int SMEM_BYTES = OFF_RING + kCrossRing * CX_BYTES + 1024;   // + alignment slack
+    static constexpr int SMEM_BYTES = OFF_OUT + 8 * 4096 + 1024;   // + alignment slack
     static constexpr uint32_t COL_S = 0, COL_O = 256;   // S_t at 128 t, O_t at 256 + 128 t
     static constexpr int THREADS = 384;
-    // 168 registers a thread at launch; the producer warpgroup drops to 56 and
-    // the two softmax warpgroups rise to 224: 2 * 128 * 224 + 128 * 56 = 384 * 168
-    static constexpr int REGS_SOFTMAX = 224, REGS_PRODUCER = 56;
+    // 168 registers a thread at launch; the producer warpgroup drops to 40 and
+    // the two softmax warpgroups rise to 232: 2 * 128 * 232 + 128 * 40 = 384 * 168
+    static constexpr int REGS_SOFTMAX = 232, REGS_PRODUCER = 40;
 };
 
 enum : int {
@@ -164,6 +161,17 @@ __device__ __forceinline__ void drop_unless(uint32_t &s, uint32_t keep) {
         "@p mov.b32 %0, 0xff800000;\n\t}" : "+r"(s) : "r"(keep));
 }
 
+__device__ __forceinline__ int lane_now() {
+    int v;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(v));
+    return v;
+}
+__device__ __forceinline__ int threadIdx_x_now() {
+    int v;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(v));
+    return v;
+}
+
 // 2^x for two lanes on the FMA and integer pipes: x = j + f with j = rint(x)
 // and |f| <= 1/2, 2^f as a polynomial of degree 4 fitted for the least maximum
 // relative error on [-1/2, 1/2] (2.6e-6, below every rounding of P and small
@@ -213,17 +221,20 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + CB_COUNT);
-    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    unsigned long long *units_s = reinterpret_cast<unsigned long long *>(bars + CB_COUNT + 2);
-    int *table = reinterpret_cast<int *>(smem + C::OFF_PLAN + CP_TABLE);
-    const uint32_t plan = smem_u32(smem + C::OFF_PLAN);
+    // static, so that their addresses take no registers
+    __shared__ __align__(64) uint64_t bars[CB_COUNT];
+    __shared__ __align__(16) int ring_s[kCrossRing * CX_BYTES / 4];
+    __shared__ int plan_s[2 + kCrossTable + 1];
+    __shared__ int flags_s[4];                    // abort; last of its rows, per tile; TMEM address
+    __shared__ unsigned long long units_s;
+    volatile int *abort = flags_s;
+    int *table = plan_s + CP_TABLE / 4;
+    const uint32_t plan = smem_u32(plan_s);
 
     // ---- the boundaries, checked by every CTA; the work they make
     const int stride = cross_stride(p.nseg), entries = (p.nseg + stride - 1) / stride;
     int chunk = 1 << 24;   // more than any segment has: no split
-    if (tid == 0) *units_s = 0;
+    if (tid == 0) units_s = 0;
     int bad = 0;
     unsigned long long units = 0;
     for (int i = tid; i <= p.nseg; i += C::THREADS) {
@@ -242,9 +253,9 @@ __global__ void __launch_bounds__(384, 1)
         return;
     }
     if (p.split) {
-        if (units) atomicAdd(units_s, units);
+        if (units) atomicAdd(&units_s, units);
         __syncthreads();
-        const unsigned long long all = *units_s * static_cast<unsigned>(p.heads_blocks);
+        const unsigned long long all = units_s * static_cast<unsigned>(p.heads_blocks);
         chunk = static_cast<int>(max((all + kCrossItems - 1) / kCrossItems,
                                      static_cast<unsigned long long>(kCrossMinChunk)));
     }
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(384, 1)
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(tmem_slot, 512);
+        tmem_alloc(reinterpret_cast<uint32_t *>(flags_s + 3), 512);
         tmem_relinquish();
     }
     if (warp == 10 && lane == 0) {
@@ -312,11 +323,10 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = static_cast<uint32_t>(lds32(smem_u32(flags_s + 3)));
 
-    const uint32_t bar0 = smem_u32(smem) + C::OFF_BAR, abort_at = bar0 + CB_COUNT * 8 + 4;
-    const uint32_t last_at = abort_at + 4;   // [2]
-    const uint32_t ring = smem_u32(smem) + C::OFF_RING;
+    const uint32_t bar0 = smem_u32(bars), abort_at = smem_u32(flags_s), last_at = abort_at + 4;
+    const uint32_t ring = smem_u32(ring_s);
     auto wait = [&](int bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_at(bar0 + bar * 8, parity, abort_at));
     };
@@ -595,9 +605,10 @@ __global__ void __launch_bounds__(384, 1)
             // Two copies of the code, so that only one of them pays for the masking.
             auto softmax_tile = [&](auto part, int keys, int j) {
                 uint32_t s[128];
-#pragma unroll
-                for (int i = 0; i < 128; i += 16)
-                    tmem_ld16(tS + i, *reinterpret_cast<uint32_t(*)[16]>(&s[i]));
+                tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
                 tmem_wait_ld();
                 if constexpr (decltype(part)::value) {
                     uint32_t any = 0;
@@ -717,6 +728,10 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!ok && lane == 0) give_up(abort, p.status);
             const int rows = min(lds32(xs + CX_Q_LEFT) - t * p.tokens, p.tokens) * p.hp;
+            // read anew, or what depends on them alone (a dozen addresses) is kept in
+            // registers through the score loop, which then spills
+            const int lane = lane_now(), warp = threadIdx_x_now() >> 5;
+            const int r = (warp & 3) * 32 + lane;
             const bool row_ok = r < rows;
             const int tok = r / p.hp, splits = lds32(xs + CX_SPLITS);
             const int qrow = lds32(xs + CX_Q0) + t * p.tokens + tok, head = lds32(xs + CX_HEAD) * p.hp + r - tok * p.hp;
@@ -731,21 +746,21 @@ __global__ void __launch_bounds__(384, 1)
                 const uint32_t out = smem_u32(smem) + C::OFF_OUT + warp * 4096;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 64) {
-                    uint32_t o[64];
-                    if (n_kv > 0) {
-                        tmem_ld32(tO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-                        tmem_ld32(tO + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = l > 0.0f ? pack2<T>(__uint_as_float(o[2 * i]) * inv_l,
-                                                   __uint_as_float(o[2 * i + 1]) * inv_l) : 0u;
                     __syncwarp();
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t o[16];
+                        if (n_kv > 0) tmem_ld16(tO + c + q * 16, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sts128(out + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1],
-                               o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            o[i] = l > 0.0f ? pack2<T>(__uint_as_float(o[2 * i]) * inv_l,
+                                                       __uint_as_float(o[2 * i + 1]) * inv_l) : 0u;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sts128(out + lane * 128 + (((q * 2 + i) ^ (lane & 7)) << 4), o[4 * i],
+                                   o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
