@@ -172,6 +172,15 @@ __device__ __forceinline__ int threadIdx_x_now() {
     return v;
 }
 
+// (y0, y1) = (x0, x1) * s, lane-wise, s a packed pair
+__device__ __forceinline__ void fmul2(float &y0, float &y1, float x0, float x1, uint64_t s) {
+    asm("{\n\t.reg .b64 xa, da;\n\t"
+        "mov.b64 xa, {%2, %3};\n\t"
+        "mul.rn.f32x2 da, xa, %4;\n\t"
+        "mov.b64 {%0, %1}, da;\n\t}"
+        : "=f"(y0), "=f"(y1) : "f"(x0), "f"(x1), "l"(s));
+}
+
 // 2^x for two lanes on the FMA and integer pipes: x = j + f with j = rint(x)
 // and |f| <= 1/2, 2^f as a polynomial of degree 4 fitted for the least maximum
 // relative error on [-1/2, 1/2] (2.6e-6, below every rounding of P and small
@@ -662,15 +671,16 @@ __global__ void __launch_bounds__(384, 1)
                     m = m_new;
                 }
                 const float nm = P_SHIFT - m;
-                uint32_t pk[64];
                 uint64_t acc0 = 0, acc1 = 0;
                 const uint64_t s2 = f2_splat(sl2), n2 = f2_splat(nm);
-                // P of keys [64 h, 64 h + 64), three pairs of eight on the FMA pipe
-                auto exp_half = [&](const int h) {
+                // P of keys [32 h, 32 h + 32), three pairs of eight on the FMA pipe
+                auto exp_part = [&](const int h) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int c = 32 * h; c < 32 * h + 32; ++c) {
+                    for (int c = 0; c < 16; ++c) {
                         float x0, x1, p0, p1;
-                        ffma2(x0, x1, __uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), s2, n2);
+                        ffma2(x0, x1, __uint_as_float(s[32 * h + 2 * c]),
+                              __uint_as_float(s[32 * h + 2 * c + 1]), s2, n2);
                         if ((c & 7) >= 5) {
                             cross_exp2_fma2(p0, p1, x0, x1);
                         } else {
@@ -680,13 +690,14 @@ __global__ void __launch_bounds__(384, 1)
                         if (c & 1) fadd2(acc1, p0, p1); else fadd2(acc0, p0, p1);
                         pk[c] = pack2<T>(p0, p1);
                     }
+                    tmem_st16(tS + 16 * h, pk);
                 };
                 if (two) {
                     ok = take_turn();
                     if (!ok) return;
                 }
-                exp_half(0);
-                tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                exp_part(0);
+                exp_part(1);
                 if (__any_sync(0xffffffffu, need)) {
                     // O holds P V up to the tile before; rescale it before P is released
 #pragma unroll
@@ -703,10 +714,10 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(bar_t + CB_P1 * 8);
-                exp_half(1);
+                exp_part(2);
+                exp_part(3);
                 if (two) give_turn();
                 l += f2_sum(acc0) + f2_sum(acc1);
-                tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -737,38 +748,51 @@ __global__ void __launch_bounds__(384, 1)
             const int qrow = lds32(xs + CX_Q0) + t * p.tokens + tok, head = lds32(xs + CX_HEAD) * p.hp + r - tok * p.hp;
             if (splits == 1) {
                 if (!ok || !active) continue;
-                const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
+                // a row without keys: O is 0 or, without a single key tile, not there
+                const uint64_t inv2 = f2_splat(l > 0.0f ? 1.0f / l : 0.0f);
                 // 64 channels at a time through shared memory (16-byte pieces, their
                 // place exclusive-or'ed with the row), so that a store writes four
-                // whole 128-byte lines; 16 bytes of 32 rows at a time cost 4 to 5
-                // thousand cycles a tile (8 now, 1 for D = 64) and half-written sectors
+                // whole 128-byte lines; 16 bytes of each of 32 rows at a time took 4 to
+                // 5 thousand cycles a tile and left sectors half written
                 const int64_t at = row_ok ? qrow * p.ldo + static_cast<int64_t>(head) * D : -1;
                 const uint32_t out = smem_u32(smem) + C::OFF_OUT + warp * 4096;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 64) {
                     __syncwarp();
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t o[16];
-                        if (n_kv > 0) tmem_ld16(tO + c + q * 16, o);
+                    for (int q = 0; q < 64; q += 32) {
+                        uint32_t o[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0u;
+                        if (n_kv > 0) tmem_ld32(tO + c + q, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            o[i] = l > 0.0f ? pack2<T>(__uint_as_float(o[2 * i]) * inv_l,
-                                                       __uint_as_float(o[2 * i + 1]) * inv_l) : 0u;
+                        for (int i = 0; i < 16; ++i) {
+                            float y0, y1;
+                            fmul2(y0, y1, __uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]), inv2);
+                            o[i] = pack2<T>(y0, y1);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            sts128(out + lane * 128 + (((q * 2 + i) ^ (lane & 7)) << 4), o[4 * i],
+                        for (int i = 0; i < 4; ++i)
+                            sts128(out + lane * 128 + (((q / 8 + i) ^ (lane & 7)) << 4), o[4 * i],
                                    o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     __syncwarp();
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 8; i0 += 8) {   // loads, then stores: their latencies overlap
+                        uint4 v[8];
+                        int64_t row_at[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i * 4 + lane / 8, piece = lane & 7;
-                        const int64_t row_at = __shfl_sync(0xffffffffu, at, rr);
-                        const uint4 v = lds128(out + rr * 128 + ((piece ^ (rr & 7)) << 4));
-                        if (row_at >= 0)
-                            *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + row_at + c + piece * 8) = v;
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = (i0 + i) * 4 + lane / 8;
+                            v[i] = lds128(out + rr * 128 + (((lane ^ rr) & 7) << 4));
+                            row_at[i] = __shfl_sync(0xffffffffu, at, rr);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (row_at[i] >= 0)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + row_at[i] + c +
+                                                           (lane & 7) * 8) = v[i];
                     }
                 }
                 if (row_ok && p.lse != nullptr)
