@@ -386,6 +386,16 @@ __global__ void __launch_bounds__(384, 1)
             item_done(n);
             if (n_kv < 0) break;
             for (int j = 0; ok && j < n_kv; ++j) {
+                const int s = nk & 1;
+                ok = wait(CB_KEMPTY + s, ((nk >> 1) & 1) ^ 1);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(&bars[CB_KFULL + s], C::TILE_BYTES);
+                    cross_load(smem + C::OFF_K + s * C::TILE_BYTES, &tmK, &bars[CB_KFULL + s],
+                               C::NBOX, kv_head, k0 + j * 128);
+                }
+                ++nk;
+                // behind the keys, whose room is free earlier
                 if (j == 0)
                     for (int t = 0; ok && t < n_t; ++t) {
                         ok = wait(CB_QEMPTY + t, (nq[t] & 1) ^ 1);
@@ -398,15 +408,6 @@ __global__ void __launch_bounds__(384, 1)
                         ++nq[t];
                     }
                 if (!ok) break;
-                const int s = nk & 1;
-                ok = wait(CB_KEMPTY + s, ((nk >> 1) & 1) ^ 1);
-                if (!ok) break;
-                if (leader) {
-                    mbar_arrive_expect_tx(&bars[CB_KFULL + s], C::TILE_BYTES);
-                    cross_load(smem + C::OFF_K + s * C::TILE_BYTES, &tmK, &bars[CB_KFULL + s],
-                               C::NBOX, kv_head, k0 + j * 128);
-                }
-                ++nk;
                 ok = wait(CB_VEMPTY + s, ((nv >> 1) & 1) ^ 1);
                 if (!ok) break;
                 if (leader) {
@@ -490,11 +491,13 @@ __global__ void __launch_bounds__(384, 1)
             }
         };
         auto issue_pv = [&](int t, int stage, int from, int to, bool add) {
-            const uint64_t dv = dV + static_cast<uint64_t>((stage * C::TILE_BYTES) >> 4);
-            for (int kk = from; kk < to; ++kk)
-                umma_ts_w(tmem + C::COL_O + t * 128, tmem + C::COL_S + t * 128 + kk * 8,
-                          dv + static_cast<uint64_t>((kk * 2048) >> 4), IDESC_O,
-                          (add || kk > 0) ? 1u : 0u, leader);
+            const uint64_t dv = dV + static_cast<uint64_t>((stage * C::TILE_BYTES + from * 2048) >> 4);
+            const uint32_t o = tmem + C::COL_O + t * 128, a = tmem + C::COL_S + t * 128 + from * 8;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                if (from + kk < to)
+                    umma_ts_w(o, a + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), IDESC_O,
+                              (add || kk > 0) ? 1u : 0u, leader);
         };
         int nq[2] = {0, 0}, g[2] = {0, 0};   // items and key tiles of each query tile so far
         int nkv = 0;                         // key tiles so far
@@ -519,33 +522,38 @@ __global__ void __launch_bounds__(384, 1)
                 ++nq[t];
             }
             for (int j = 0; ok && j < n_kv; ++j, ++nkv) {
+                // everything but P is waited for ahead of P, whose arrival is what the
+                // tensor cores wait for
                 const int s = nkv & 1, keys = keys_in(k_left, j), n16 = (keys + 15) / 16;
-                const bool more = j + 1 < n_kv, fix = p.mask != nullptr || keys % 16 != 0;
+                const bool more = j + 1 < n_kv;
+                ok = mma_wait(CB_VFULL + s, (nkv >> 1) & 1);
+                if (ok && (p.mask != nullptr || keys % 16 != 0)) {
+                    ok = mma_wait(CB_VFIX + s, (fixes >> s) & 1);
+                    fixes ^= 1u << s;
+                }
+                const int next_keys = keys_in(k_left, j + 1);
                 for (int t = 0; ok && t < n_t; ++t) {
-                    ok = mma_wait(CB_P1 + t, g[t] & 1) && mma_wait(CB_VFULL + s, (nkv >> 1) & 1);
-                    if (ok && fix && t == 0) ok = mma_wait(CB_VFIX + s, (fixes >> s) & 1);
+                    ok = mma_wait(CB_P1 + t, g[t] & 1);
                     if (!ok) break;
-                    issue_pv(t, s, 0, min(n16, 4), j > 0);
-                    ok = mma_wait(CB_P2 + t, g[t] & 1);
+                    issue_pv(t, s, 0, n16, j > 0);
+                    if (more && t == 0) ok = mma_wait(CB_KFULL + (s ^ 1), ((nkv + 1) >> 1) & 1);
+                    ok = ok && mma_wait(CB_P2 + t, g[t] & 1);
                     if (!ok) break;
                     issue_pv(t, s, 4, n16, true);
-                    umma_commit_w(&bars[CB_VEMPTY + s], leader);
-                    if (n_t == 1) umma_commit_w(&bars[CB_VEMPTY + s], leader);
                     if (more) {
-                        const int s1 = (nkv + 1) & 1;
-                        ok = mma_wait(CB_KFULL + s1, ((nkv + 1) >> 1) & 1);
-                        if (!ok) break;
-                        issue_s(t, s1, keys_in(k_left, j + 1));
+                        umma_commit_w(&bars[CB_VEMPTY + s], leader);
+                        issue_s(t, s ^ 1, next_keys);
                         umma_commit_w(&bars[CB_SFULL + t], leader);
-                        umma_commit_w(&bars[CB_KEMPTY + s1], leader);
-                        if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + s1], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + (s ^ 1)], leader);
+                        if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (s ^ 1)], leader);
                         if (j + 2 == n_kv) umma_commit_w(&bars[CB_QEMPTY + t], leader);
                     } else {
                         umma_commit_w(&bars[CB_OFULL + t], leader);
+                        umma_commit_w(&bars[CB_VEMPTY + s], leader);
                     }
+                    if (n_t == 1) umma_commit_w(&bars[CB_VEMPTY + s], leader);
                     ++g[t];
                 }
-                if (fix) fixes ^= 1u << s;
             }
         }
         if (!ok) {

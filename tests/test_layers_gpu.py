@@ -341,6 +341,16 @@ def test_cross(lq, lk, Hq, Hk, D, dtype):
     _check_cross(q, k, v, cu_q, cu_k, o, lse, D ** -0.5, None, "o")
 
 
+@pytest.mark.parametrize("lk", [40, 128, 200, 300])
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "fp16")])
+def test_cross_many_items_a_cta(lk, D, dtype):
+    """Several times as many items as SMs, with one to three key tiles each."""
+    lq = [3700, 1, 200]
+    q, k, v, cu_q, cu_k = _cross_case(lq, [lk, lk, 1], 48, 48, D, dtype)
+    o, lse = _run_cross(q, k, v, cu_q, cu_k, lq, [lk, lk, 1])
+    _check_cross(q, k, v, cu_q, cu_k, o, lse, D ** -0.5, None, "o")
+
+
 @pytest.mark.parametrize("group", [3, 5, 7, 16, 56, 100, 130])
 @pytest.mark.parametrize("lq,lk", [([1, 1], [900, 3]), ([90, 33], [70, 300])])
 def test_cross_group_sizes(group, lq, lk):
