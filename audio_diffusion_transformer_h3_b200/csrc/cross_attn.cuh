@@ -22,12 +22,12 @@
 //   warp 10     TMA producer.
 //   warp 11     finds the items (a search over the segments) ahead of the others
 //               and hands them over in a ring of four.
-// A key tile's products stop at its last key (in steps of 16). Items with no
-// more rows than one tile leave the second tile out.
+// A key tile's products stop at its last key (in steps of 16).
 //
-// Few rows: the keys of a segment are split into chunks so that all SMs read;
-// each item leaves its unnormalised O, m and l in fp32 and the last item of its
-// rows to finish joins them in the chunks' order.
+// Few rows: an item with no more rows than one tile gives both tiles the same
+// rows and every other key tile, and the keys of a segment are split into
+// chunks so that all SMs read. Each tile then leaves its unnormalised O, m and
+// l in fp32, and cross_join_kernel adds a row's parts up in their order.
 //
 // Every wait is bounded; one that gives up sets H3_ERR_DEVICE_TIMEOUT, stops
 // the CTA, and leaves TMEM and shared memory only after the copies and MMAs in
@@ -51,8 +51,8 @@ struct CrossParams {
     int32_t hp, tokens, heads_blocks;   // heads and tokens of a tile, Hq / hp
     int32_t split;                      // 1: keys may be split
     float scale_log2;
-    int *arrived;                       // [item], zero at launch (split)
-    float *parts;                       // [item][slot_rows][D + 2]
+    float *parts;                       // [item][tile][slot_rows][m, l, O]
+    int2 *rows;                         // [token][query head]: first part, parts (split)
     int32_t slot_rows;
 };
 
@@ -71,8 +71,12 @@ enum : int {
     CX_SPLITS = 24,    // chunks that these rows' keys are split into
     CX_GROUP = 28,     // item number of the first of them
     CX_ITEM = 32,      // item number
+    CX_MODE = 36,      // CM_*
     CX_BYTES = 48
 };
+// How an item uses its two tiles: one only; the first and the second half of its
+// rows; the same rows for the even and the odd key tiles.
+enum : int { CM_ONE = 0, CM_ROWS = 1, CM_KEYS = 2 };
 constexpr int kCrossRing = 4;
 
 template <int D>
@@ -94,7 +98,7 @@ enum : int {
     CB_QFULL = 0, CB_QEMPTY = 2, CB_KFULL = 4, CB_KEMPTY = 6, CB_VFULL = 8, CB_VEMPTY = 10,
     CB_VFIX = 12, CB_SFULL = 14, CB_P1 = 16, CB_P2 = 18, CB_OFULL = 20, CB_DRAIN = 22,
     CB_TURN = 24,   // CB_TURN * 8 is a multiple of 64
-    CB_IFULL = 32, CB_IEMPTY = 36, CB_JOIN = 40, CB_COUNT = 42
+    CB_IFULL = 32, CB_IEMPTY = 36, CB_COUNT = 40
 };
 
 // The plan of a launch in shared memory, from one address on: the key tiles of a
@@ -135,7 +139,9 @@ __device__ __forceinline__ void cross_find_item(const CrossParams &p, uint32_t p
     const int head = it - unit * p.heads_blocks;
     const int q0 = p.cu_q[s] + block * 2 * p.tokens, k0 = p.cu_k[s] + first * 128;
     sts32(to + CX_Q0, q0);
-    sts32(to + CX_Q_LEFT, min(p.cu_q[s + 1] - q0, 2 * p.tokens));
+    const int q_left = min(p.cu_q[s + 1] - q0, 2 * p.tokens);
+    sts32(to + CX_Q_LEFT, q_left);
+    sts32(to + CX_MODE, q_left > p.tokens ? CM_ROWS : (p.split && tiles > 1 ? CM_KEYS : CM_ONE));
     sts32(to + CX_HEAD, head);
     sts32(to + CX_K0, k0);
     sts32(to + CX_K_LEFT, p.cu_k[s + 1] - k0);
@@ -234,7 +240,7 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(64) uint64_t bars[CB_COUNT];
     __shared__ __align__(16) int ring_s[kCrossRing * CX_BYTES / 4];
     __shared__ int plan_s[2 + kCrossTable + 1];
-    __shared__ int flags_s[4];                    // abort; last of its rows, per tile; TMEM address
+    __shared__ int flags_s[2];                    // abort, TMEM address
     __shared__ unsigned long long units_s;
     volatile int *abort = flags_s;
     int *table = plan_s + CP_TABLE / 4;
@@ -291,7 +297,6 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&bars[CB_P1 + s], 4);
             mbar_init(&bars[CB_P2 + s], 4);
             mbar_init(&bars[CB_OFULL + s], 1);
-            mbar_init(&bars[CB_JOIN + s], 4);
         }
         mbar_init(&bars[CB_DRAIN], 1);
         for (int i = 0; i < kCrossRing; ++i) {
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(384, 1)
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(reinterpret_cast<uint32_t *>(flags_s + 3), 512);
+        tmem_alloc(reinterpret_cast<uint32_t *>(flags_s + 1), 512);
         tmem_relinquish();
     }
     if (warp == 10 && lane == 0) {
@@ -332,9 +337,9 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = static_cast<uint32_t>(lds32(smem_u32(flags_s + 3)));
+    const uint32_t tmem = static_cast<uint32_t>(lds32(smem_u32(flags_s + 1)));
 
-    const uint32_t bar0 = smem_u32(bars), abort_at = smem_u32(flags_s), last_at = abort_at + 4;
+    const uint32_t bar0 = smem_u32(bars), abort_at = smem_u32(flags_s);
     const uint32_t ring = smem_u32(ring_s);
     auto wait = [&](int bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_at(bar0 + bar * 8, parity, abort_at));
@@ -349,6 +354,11 @@ __global__ void __launch_bounds__(384, 1)
     };
     // keys of key tile j
     auto keys_in = [](int k_left, int j) { return min(k_left - j * 128, 128); };
+    // which of a key tile's 32 keys from `c` on count, for all lanes
+    auto keys_valid = [&](int k0, int keys, int c) {
+        c += lane;
+        return __ballot_sync(0xffffffffu, c < keys && (p.mask == nullptr || p.mask[k0 + c] != 0));
+    };
 
     if (warp == 11) {
         // ============================ items ===================================
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t x = ring + (n % kCrossRing) * CX_BYTES;
             const int n_kv = lds32(x + CX_N_KV), head = lds32(x + CX_HEAD) * p.hp;
             const int kv_head = head / (p.Hq / p.Hk), q0 = lds32(x + CX_Q0), k0 = lds32(x + CX_K0);
-            const int n_t = lds32(x + CX_Q_LEFT) > p.tokens ? 2 : 1;
+            const int n_t = lds32(x + CX_MODE) == CM_ROWS ? 2 : 1;
             item_done(n);
             if (n_kv < 0) break;
             for (int j = 0; ok && j < n_kv; ++j) {
@@ -443,20 +453,29 @@ __global__ void __launch_bounds__(384, 1)
             if (n_kv < 0) break;
             for (int j = 0; ok && j < n_kv; ++j, ++nv) {
                 const int keys = keys_in(k_left, j), s = nv & 1, rows = (keys + 15) / 16 * 16;
+                const bool fix = p.mask != nullptr || keys % 16 != 0;
+                uint32_t valid[4] = {0, 0, 0, 0};
+                if (fix) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) valid[i] = keys_valid(k0 + j * 128, keys, i * 32);
+                }
                 // every phase is waited for, those of tiles that need nothing too: a
                 // parity tells a phase from its neighbours only
                 ok = wait(CB_VFULL + s, (nv >> 1) & 1);
                 if (!ok) break;
-                if (p.mask == nullptr && keys % 16 == 0) continue;
+                if (!fix) continue;
                 uint8_t *v = smem + C::OFF_V + s * C::TILE_BYTES;
-                // four rows a step, eight lanes a row; without a mask the last step of 16 only
-                for (int r0 = p.mask == nullptr ? rows - 16 : 0; r0 < rows; r0 += 4) {
-                    const int r = r0 + lane / 8;
-                    const bool counts = r < keys && (p.mask == nullptr || p.mask[k0 + j * 128 + r] != 0);
-                    if (!counts)
-                        for (int b = 0; b < C::NBOX; ++b)
-                            *reinterpret_cast<uint4 *>(v + b * C::BOX_BYTES + r * 128 +
-                                                       (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                // four rows a step, eight lanes a row
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    for (int r0 = 0; r0 < 32 && i * 32 + r0 < rows; r0 += 4) {
+                        if (((valid[i] >> r0) & 15u) == 15u) continue;
+                        const int r = i * 32 + r0 + lane / 8;
+                        if (!((valid[i] >> (r & 31)) & 1u))
+                            for (int b = 0; b < C::NBOX; ++b)
+                                *reinterpret_cast<uint4 *>(v + b * C::BOX_BYTES + r * 128 +
+                                                           (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -479,9 +498,9 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             return r;
         };
-        auto issue_s = [&](int t, int stage, int keys) {
+        auto issue_s = [&](int t, int tq, int stage, int keys) {
             const uint32_t n16 = static_cast<uint32_t>((keys + 15) / 16);
-            const uint64_t dq = dQ + static_cast<uint64_t>((t * C::TILE_BYTES) >> 4);
+            const uint64_t dq = dQ + static_cast<uint64_t>((tq * C::TILE_BYTES) >> 4);
             const uint64_t dk = dK + static_cast<uint64_t>((stage * C::TILE_BYTES) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(384, 1)
                     umma_ts_w(o, a + kk * 8, dv + static_cast<uint64_t>((kk * 2048) >> 4), IDESC_O,
                               (add || kk > 0) ? 1u : 0u, leader);
         };
-        int nq[2] = {0, 0}, g[2] = {0, 0};   // items and key tiles of each query tile so far
+        uint32_t nq = 0, g = 0;              // parities of the next Q and P phases, a bit a tile
         int nkv = 0;                         // key tiles so far
         uint32_t fixes = 0;                  // parity of the next VFIX phase, a bit a stage
         bool ok = true;
@@ -508,18 +527,56 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             const uint32_t x = ring + (n % kCrossRing) * CX_BYTES;
             const int n_kv = lds32(x + CX_N_KV), k_left = lds32(x + CX_K_LEFT);
-            const int n_t = lds32(x + CX_Q_LEFT) > p.tokens ? 2 : 1;
+            const bool keys_mode = lds32(x + CX_MODE) == CM_KEYS;
+            const int n_t = lds32(x + CX_MODE) == CM_ROWS ? 2 : 1;
             item_done(n);
             if (n_kv < 0) break;
+            if (keys_mode) {
+                ok = mma_wait(CB_QFULL, nq & 1);
+                nq ^= 1u;
+                for (int j = -2; ok && j < n_kv; ++j) {   // key tile j: values of j, scores of j + 2
+                    const int t = j & 1, s = nkv & 1;
+                    if (j >= 0) {
+                        const int keys = keys_in(k_left, j), n16 = (keys + 15) / 16;
+                        ok = mma_wait(CB_VFULL + s, (nkv >> 1) & 1);
+                        if (ok && (p.mask != nullptr || keys % 16 != 0)) {
+                            ok = mma_wait(CB_VFIX + s, (fixes >> s) & 1);
+                            fixes ^= 1u << s;
+                        }
+                        ok = ok && mma_wait(CB_P1 + t, (g >> t) & 1);
+                        if (!ok) break;
+                        issue_pv(t, s, 0, n16, j >= 2);
+                        ok = mma_wait(CB_P2 + t, (g >> t) & 1);
+                        if (!ok) break;
+                        issue_pv(t, s, 4, n16, true);
+                        umma_commit_w(&bars[CB_VEMPTY + s], leader);
+                        umma_commit_w(&bars[CB_VEMPTY + s], leader);
+                        if (j + 2 >= n_kv) umma_commit_w(&bars[CB_OFULL + t], leader);
+                        g ^= 1u << t;
+                        ++nkv;
+                    }
+                    if (j + 2 < n_kv) {
+                        const int at = j < 0 ? nkv + j + 2 : nkv + 1;   // = this item's key tile j + 2
+                        ok = mma_wait(CB_KFULL + (at & 1), (at >> 1) & 1);
+                        if (!ok) break;
+                        issue_s(t, 0, at & 1, keys_in(k_left, j + 2));
+                        umma_commit_w(&bars[CB_SFULL + t], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + (at & 1)], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + (at & 1)], leader);
+                        if (j + 3 == n_kv) umma_commit_w(&bars[CB_QEMPTY], leader);
+                    }
+                }
+                continue;
+            }
             for (int t = 0; ok && n_kv > 0 && t < n_t; ++t) {
-                ok = mma_wait(CB_QFULL + t, nq[t] & 1) && mma_wait(CB_KFULL + (nkv & 1), (nkv >> 1) & 1);
+                ok = mma_wait(CB_QFULL + t, (nq >> t) & 1) && mma_wait(CB_KFULL + (nkv & 1), (nkv >> 1) & 1);
                 if (!ok) break;
-                issue_s(t, nkv & 1, keys_in(k_left, 0));
+                issue_s(t, t, nkv & 1, keys_in(k_left, 0));
                 umma_commit_w(&bars[CB_SFULL + t], leader);
                 umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
                 if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
                 if (n_kv == 1) umma_commit_w(&bars[CB_QEMPTY + t], leader);
-                ++nq[t];
+                nq ^= 1u << t;
             }
             for (int j = 0; ok && j < n_kv; ++j, ++nkv) {
                 // everything but P is waited for ahead of P, whose arrival is what the
@@ -533,16 +590,16 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 const int next_keys = keys_in(k_left, j + 1);
                 for (int t = 0; ok && t < n_t; ++t) {
-                    ok = mma_wait(CB_P1 + t, g[t] & 1);
+                    ok = mma_wait(CB_P1 + t, (g >> t) & 1);
                     if (!ok) break;
                     issue_pv(t, s, 0, n16, j > 0);
                     if (more && t == 0) ok = mma_wait(CB_KFULL + (s ^ 1), ((nkv + 1) >> 1) & 1);
-                    ok = ok && mma_wait(CB_P2 + t, g[t] & 1);
+                    ok = ok && mma_wait(CB_P2 + t, (g >> t) & 1);
                     if (!ok) break;
                     issue_pv(t, s, 4, n16, true);
                     if (more) {
                         umma_commit_w(&bars[CB_VEMPTY + s], leader);
-                        issue_s(t, s ^ 1, next_keys);
+                        issue_s(t, t, s ^ 1, next_keys);
                         umma_commit_w(&bars[CB_SFULL + t], leader);
                         umma_commit_w(&bars[CB_KEMPTY + (s ^ 1)], leader);
                         if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (s ^ 1)], leader);
@@ -552,7 +609,7 @@ __global__ void __launch_bounds__(384, 1)
                         umma_commit_w(&bars[CB_VEMPTY + s], leader);
                     }
                     if (n_t == 1) umma_commit_w(&bars[CB_VEMPTY + s], leader);
-                    ++g[t];
+                    g ^= 1u << t;
                 }
             }
         }
@@ -566,12 +623,11 @@ __global__ void __launch_bounds__(384, 1)
         // ============================ softmax / output ========================
         reg_alloc<C::REGS_SOFTMAX>();
         const int t = warp >> 2;                 // query tile of this warpgroup
-        const int r = tid & 127;                 // row of the tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + C::COL_S + t * 128;
         const uint32_t tO = tS + (C::COL_O - C::COL_S);
         const float sl2 = p.scale_log2;
-        uint32_t par = 0;   // parities of the next phases: 1 S, 2 O, 4 turn, 8 join
+        uint32_t par = 0;   // parities of the next phases: 1 S, 2 O, 4 turn
         // Barrier addresses from few registers: those of tile t, and this sub-partition's
         // turns. Tile 0 waits for tile 1's last key tile in turn, tile 1 for tile 0's same
         // one; each gives on the other's barrier, 32 bytes (of 64) away.
@@ -598,13 +654,20 @@ __global__ void __launch_bounds__(384, 1)
                 break;
             }
             const uint32_t xs = ring + (n % kCrossRing) * CX_BYTES;   // read again after the loop
-            const int n_kv = lds32(xs + CX_N_KV), k_left = lds32(xs + CX_K_LEFT);
+            const int mode = lds32(xs + CX_MODE);
+            int n_kv = lds32(xs + CX_N_KV), k_left = lds32(xs + CX_K_LEFT);
             if (n_kv < 0) break;
-            const bool two = lds32(xs + CX_Q_LEFT) > p.tokens;
-            if (t == 1 && !two) continue;
+            if (mode == CM_ONE && t == 1) continue;
+            const bool two = mode == CM_ROWS;
+            int step = 128;   // keys from one key tile of this query tile to its next
+            if (mode == CM_KEYS) {
+                step = 256;
+                k_left -= t * 128;
+                n_kv = (n_kv + 1 - t) >> 1;
+            }
             // a warp without rows only signals
             const bool active = (warp & 3) * 32 <
-                                min(lds32(xs + CX_Q_LEFT) - t * p.tokens, p.tokens) * p.hp;
+                                min(lds32(xs + CX_Q_LEFT) - (two ? t * p.tokens : 0), p.tokens) * p.hp;
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; ok && !active && j < n_kv; ++j) {
                 ok = wait_t(CB_SFULL, par & 1);
@@ -621,6 +684,16 @@ __global__ void __launch_bounds__(384, 1)
             // One key tile of this warp's rows, `keys` of them left; `part`: not all count.
             // Two copies of the code, so that only one of them pays for the masking.
             auto softmax_tile = [&](auto part, int keys, int j) {
+                uint32_t valid[4];
+                if constexpr (decltype(part)::value) {
+                    const int k0 = lds32(xs + CX_K0) + lds32(xs + CX_K_LEFT) - keys;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) valid[i] = keys_valid(k0, keys, i * 32);
+                }
+                ok = wait_t(CB_SFULL, par & 1);
+                par ^= 1u;
+                if (!ok) return;
+                tc_fence_after();
                 uint32_t s[128];
                 tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                 tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -628,18 +701,10 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
                 tmem_wait_ld();
                 if constexpr (decltype(part)::value) {
-                    uint32_t any = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = i * 32 + lane;
-                        const uint32_t valid = __ballot_sync(0xffffffffu, c < keys &&
-                            (p.mask == nullptr || p.mask[lds32(xs + CX_K0) + j * 128 + c] != 0));
-                        any |= valid;
-#pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            drop_unless(s[i * 32 + q], valid & (1u << q));
-                    }
-                    if (any == 0) {   // no key of this tile counts: P = 0, nothing else changes
+                    for (int q = 0; q < 128; ++q) drop_unless(s[q], valid[q >> 5] & (1u << (q & 31)));
+                    // no key of this tile counts: P = 0, nothing else changes
+                    if ((valid[0] | valid[1] | valid[2] | valid[3]) == 0) {
                         uint32_t z[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -732,11 +797,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (lane == 0) mbar_arrive_at(bar_t + CB_P2 * 8);
             };
             for (int j = 0; ok && active && j < n_kv; ++j) {
-                const int keys = k_left - j * 128;   // and more, behind the tile
-                ok = wait_t(CB_SFULL, par & 1);
-                par ^= 1u;
-                if (!ok) break;
-                tc_fence_after();
+                const int keys = k_left - j * step;   // and more, behind the tile
                 if (keys < 128 || p.mask != nullptr) softmax_tile(std::true_type{}, keys, j);
                 else softmax_tile(std::false_type{}, keys, j);
             }
@@ -746,16 +807,18 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after();
             }
             if (!ok && lane == 0) give_up(abort, p.status);
-            const int rows = min(lds32(xs + CX_Q_LEFT) - t * p.tokens, p.tokens) * p.hp;
+            const int t_first = two ? t * p.tokens : 0;   // first token of this tile
+            const int rows = min(lds32(xs + CX_Q_LEFT) - t_first, p.tokens) * p.hp;
             // read anew, or what depends on them alone (a dozen addresses) is kept in
             // registers through the score loop, which then spills
             const int lane = lane_now(), warp = threadIdx_x_now() >> 5;
             const int r = (warp & 3) * 32 + lane;
             const bool row_ok = r < rows;
-            const int tok = r / p.hp, splits = lds32(xs + CX_SPLITS);
-            const int qrow = lds32(xs + CX_Q0) + t * p.tokens + tok, head = lds32(xs + CX_HEAD) * p.hp + r - tok * p.hp;
-            if (splits == 1) {
-                if (!ok || !active) continue;
+            const int tok = r / p.hp;
+            const int qrow = lds32(xs + CX_Q0) + t_first + tok, head = lds32(xs + CX_HEAD) * p.hp + r - tok * p.hp;
+            const int parts = lds32(xs + CX_SPLITS) * (mode == CM_KEYS ? 2 : 1);
+            if (!ok || !active) continue;
+            if (parts == 1) {
                 // a row without keys: O is 0 or, without a single key tile, not there
                 const uint64_t inv2 = f2_splat(l > 0.0f ? 1.0f / l : 0.0f);
                 // 64 channels at a time through shared memory (16-byte pieces, their
@@ -806,76 +869,30 @@ __global__ void __launch_bounds__(384, 1)
                 if (row_ok && p.lse != nullptr)
                     p.lse[static_cast<int64_t>(head) * p.Nq + qrow] =
                         l > 0.0f ? (m + (log2f(l) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
+                if (p.split && row_ok)   // not among the parts
+                    p.rows[static_cast<int64_t>(qrow) * p.Hq + head] = make_int2(0, 0);
                 continue;
             }
-            // ---- one chunk of the keys: leave O, m, l; the rows' last item joins
-            const int64_t slot = static_cast<int64_t>(p.slot_rows) * (D + 2);
-            const int row0 = t * p.tokens * p.hp;     // of this tile in the slot
-            if (ok && active) {
-                float *mine = p.parts + lds32(xs + CX_ITEM) * slot + static_cast<int64_t>(row0 + r) * (D + 2);
-                if (row_ok) *reinterpret_cast<float2 *>(mine) = make_float2(m, l);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + c * 32, o);
-                    tmem_wait_ld();
-                    if (row_ok) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            *reinterpret_cast<uint2 *>(mine + 2 + c * 32 + i) = make_uint2(o[i], o[i + 1]);
-                    }
-                }
+            // ---- one of several parts of these rows: O, m and l as they are
+            const int64_t first = static_cast<int64_t>(lds32(xs + CX_ITEM)) * 2 + t;
+            float *mine = p.parts + (first * p.slot_rows + r) * (D + 2);
+            if (row_ok) {
+                *reinterpret_cast<float2 *>(mine) = make_float2(m, l);
+                // the rows' first part says where they are
+                if (lds32(xs + CX_ITEM) == lds32(xs + CX_GROUP) && (mode != CM_KEYS || t == 0))
+                    p.rows[static_cast<int64_t>(qrow) * p.Hq + head] = make_int2(
+                        static_cast<int>(first * p.slot_rows) + r, mode == CM_KEYS ? -parts : parts);
             }
-            __threadfence();
-            // the two tiles may be at different items: a count, a flag and a barrier each
-            auto meet = [&]() {
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(bar_t + CB_JOIN * 8);
-                ok = wait_t(CB_JOIN, (par >> 3) & 1) && ok;
-                par ^= 8u;
-            };
-            meet();
-            if (r == 0)
-                sts32(last_at + 4 * t, ok && lds32(abort_at) == 0 &&
-                      atomicAdd(&p.arrived[2 * lds32(xs + CX_GROUP) + t], 1) == splits - 1);
-            meet();
-            if (!ok) {
-                if (lane == 0) give_up(abort, p.status);
-                continue;
-            }
-            if (!lds32(last_at + 4 * t)) continue;
-            __threadfence();
-            for (int rr = warp & 3; rr < rows; rr += 4) {   // a warp a row
-                const float *all = p.parts + lds32(xs + CX_GROUP) * slot + static_cast<int64_t>(row0 + rr) * (D + 2);
-                const int64_t step = slot * p.heads_blocks;
-                float mm = -INFINITY;
-                for (int i = 0; i < splits; ++i) mm = fmaxf(mm, __ldcg(all + i * step));
-                float sum = 0.0f, o[D / 32];
+#pragma unroll 1
+            for (int c = 0; n_kv > 0 && c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + c, o);
+                tmem_wait_ld();
+                if (row_ok) {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
-                for (int i = 0; i < splits; ++i) {
-                    const float mi = __ldcg(all + i * step);
-                    const float wgt = mi == -INFINITY ? 0.0f : ex2_approx(mi - mm);
-                    sum = fmaf(wgt, __ldcg(all + i * step + 1), sum);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(
-                            all + i * step + 2 + c * 64 + lane * 2));
-                        o[2 * c] = fmaf(wgt, v.x, o[2 * c]);
-                        o[2 * c + 1] = fmaf(wgt, v.y, o[2 * c + 1]);
-                    }
+                    for (int i = 0; i < 16; i += 2)
+                        *reinterpret_cast<uint2 *>(mine + 2 + c + i) = make_uint2(o[i], o[i + 1]);
                 }
-                const int rt = rr / p.hp;
-                const int row = lds32(xs + CX_Q0) + t * p.tokens + rt, hh = lds32(xs + CX_HEAD) * p.hp + rr - rt * p.hp;
-                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-                T *orow = static_cast<T *>(p.o) + row * p.ldo + static_cast<int64_t>(hh) * D;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    *reinterpret_cast<uint32_t *>(orow + c * 64 + lane * 2) =
-                        pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
-                if (lane == 0 && p.lse != nullptr)
-                    p.lse[static_cast<int64_t>(hh) * p.Nq + row] =
-                        sum > 0.0f ? (mm + (log2f(sum) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
             }
         }
     }
@@ -886,6 +903,65 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Joins the parts of the rows that have several: a warp a row, lane i the weight
+// of part i, then all lanes the channels. Part i of a row lies one item's slots
+// (both tiles') behind the other or, where an item's two tiles share rows
+// (count negative), tile by tile.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p) {
+    constexpr float P_SHIFT = std::is_same<T, __half>::value ? 6.0f : 0.0f;
+    if (*p.status != 0) return;   // the main kernel has not written what is read here
+    const int lane = threadIdx.x % 32;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+    if (row >= static_cast<int64_t>(p.cu_q[p.nseg]) * p.Hq) return;
+    const int2 at = p.rows[row];
+    const bool pairs = at.y < 0;
+    const int parts = pairs ? -at.y : at.y;
+    if (parts == 0) return;
+    const int64_t tile = static_cast<int64_t>(p.slot_rows) * (D + 2);   // floats
+    const int64_t item = 2 * tile * p.heads_blocks;
+    const float *all = p.parts + static_cast<int64_t>(at.x) * (D + 2);
+    auto part = [&](int i) { return all + (pairs ? (i >> 1) * item + (i & 1) * tile : i * item); };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part(i)[0]);
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float sum = 0.0f, o[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        // a part without keys may hold no O: its weight 0 also says not to read it
+        float w = 0.0f;
+        if (i0 + lane < parts) {
+            const float2 ml = *reinterpret_cast<const float2 *>(part(i0 + lane));
+            w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+            sum = fmaf(w, ml.y, sum);
+        }
+        const int n = min(parts - i0, 32);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (wi == 0.0f) continue;
+            const float *a = part(i0 + i) + 2 + lane * 2;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const float2 v = *reinterpret_cast<const float2 *>(a + c * 64);
+                o[2 * c] = fmaf(wi, v.x, o[2 * c]);
+                o[2 * c + 1] = fmaf(wi, v.y, o[2 * c + 1]);
+            }
+        }
+    }
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int token = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(token) * p.Hq);
+    T *to = static_cast<T *>(p.o) + token * p.ldo + static_cast<int64_t>(head) * D;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+        *reinterpret_cast<uint32_t *>(to + c * 64 + lane * 2) = pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[static_cast<int64_t>(head) * p.Nq + token] =
+            sum > 0.0f ? (m + (log2f(sum) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace h3

@@ -285,12 +285,12 @@ struct CrossPlanHost {
     int64_t items;            // bound on the items without a split
     bool split;
     int64_t slots;            // bound on the items with it
-    int32_t slot_rows;
+    int32_t slot_rows;        // of one of an item's two tiles
 };
 
 // A tile takes the whole group of query heads of a key head where the group
 // fits, else single heads. The keys are split where the items alone could not
-// give each SM two and a segment may have more key tiles than a chunk has.
+// give each SM two and a segment may have more than one key tile.
 CrossPlanHost cross_plan(int64_t Nq, int32_t Hq, int32_t Hk, int32_t nseg, int32_t max_q,
                          int32_t max_k) {
     CrossPlanHost c;
@@ -299,14 +299,15 @@ CrossPlanHost cross_plan(int64_t Nq, int32_t Hq, int32_t Hk, int32_t nseg, int32
     c.tokens = 128 / c.hp;
     const int64_t two = 2 * c.tokens;
     c.items = std::min(nseg * ((max_q + two - 1) / two), Nq / two + nseg) * (Hq / c.hp);
-    c.split = c.items < h3::kCrossItems && (static_cast<int64_t>(max_k) + 127) / 128 > h3::kCrossMinChunk;
+    c.split = c.items < h3::kCrossItems && max_k > 128;
     c.slots = c.split ? c.items + h3::kCrossItems : 0;
-    c.slot_rows = static_cast<int32_t>(std::min<int64_t>(two, max_q)) * c.hp;
+    c.slot_rows = std::min(c.tokens, max_q) * c.hp;
     return c;
 }
 
-size_t cross_counter_bytes(const CrossPlanHost &c) {
-    return h3host::round_up(static_cast<size_t>(c.slots) * 8, 256);
+// Behind the status block: where each row's parts are, then the parts.
+size_t cross_rows_bytes(const CrossPlanHost &c, int64_t Nq, int32_t Hq) {
+    return c.split ? h3host::round_up(static_cast<size_t>(Nq) * Hq * 8, 256) : 0;
 }
 
 // TMA map over a [N, H, D] tensor of 16-bit elements, token stride ld, box
@@ -332,6 +333,10 @@ h3_status launch_cross(const h3::CrossParams &p, int grid, const CUtensorMap &tq
                        const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
     using C = h3::CrossCfg<D>;
     h3::cross_attn_kernel<T, D><<<grid, C::THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
+    if (p.split) {
+        const int64_t rows = static_cast<int64_t>(p.Nq) * p.Hq;   // a warp each
+        h3::cross_join_kernel<T, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
+    }
     return launched();
 }
 
@@ -473,8 +478,8 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
     if (!cross_sizes_ok(Nq, 0, Hq, Hk, nseg) || (D != 64 && D != 128) || max_q < 0 || max_k < 0)
         return 0;
     const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
-    return kStatusBytes + cross_counter_bytes(c) +
-           static_cast<size_t>(c.slots) * c.slot_rows * (D + 2) * 4;
+    return kStatusBytes + cross_rows_bytes(c, Nq, Hq) +
+           static_cast<size_t>(c.slots) * 2 * c.slot_rows * (D + 2) * 4;
 }
 
 h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk,
@@ -513,8 +518,7 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     if (!d->cross_regs_ok) return H3_ERR_UNSUPPORTED;
     const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const cudaError_t e = cudaMemsetAsync(
-        ws, 0, Nq > 0 && c.split ? kStatusBytes + cross_counter_bytes(c) : sizeof(int), cs);
+    const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), cs);
     if (e != cudaSuccess) return cuda_fail(e);
     if (Nq == 0) return H3_OK;
     h3::CrossParams p;
@@ -530,8 +534,8 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     // a scale of 0 (the mean of the values) as one that no score survives, so
     // that a masked score of -infinity stays one
     p.scale_log2 = std::max(softmax_scale * 1.4426950408889634f, 1e-30f);
-    p.arrived = reinterpret_cast<int *>(ws + kStatusBytes);
-    p.parts = reinterpret_cast<float *>(ws + kStatusBytes + cross_counter_bytes(c));
+    p.rows = reinterpret_cast<int2 *>(ws + kStatusBytes);
+    p.parts = reinterpret_cast<float *>(ws + kStatusBytes + cross_rows_bytes(c, Nq, Hq));
     p.slot_rows = c.slot_rows;
     CUtensorMap tq, tk, tv;
     if ((st = make_heads_map(&tq, q, Nq, Hq, D, ldq, c.hp, c.tokens)) != H3_OK) return st;
