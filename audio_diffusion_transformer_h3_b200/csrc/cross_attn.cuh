@@ -905,16 +905,18 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-// Joins the parts of the rows that have several: a warp a row, lane i the weight
-// of part i, then all lanes the channels. Part i of a row lies one item's slots
-// (both tiles') behind the other or, where an item's two tiles share rows
-// (count negative), tile by tile.
+// Joins the parts of the rows that have several: a block a row, every fourth part
+// a warp, lane i the weight of its warp's i-th, then all lanes the channels; the
+// warps' sums in the warps' order. Part i of a row lies one item's slots (both
+// tiles') behind the other or, where an item's two tiles share rows (count
+// negative), tile by tile.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p) {
     constexpr float P_SHIFT = std::is_same<T, __half>::value ? 6.0f : 0.0f;
+    __shared__ float m_s[4], sum_s[4], o_s[4][D];
     if (*p.status != 0) return;   // the main kernel has not written what is read here
-    const int lane = threadIdx.x % 32;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t row = blockIdx.x;
     if (row >= static_cast<int64_t>(p.cu_q[p.nseg]) * p.Hq) return;
     const int2 at = p.rows[row];
     const bool pairs = at.y < 0;
@@ -925,25 +927,29 @@ __global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p) {
     const float *all = p.parts + static_cast<int64_t>(at.x) * (D + 2);
     auto part = [&](int i) { return all + (pairs ? (i >> 1) * item + (i & 1) * tile : i * item); };
     float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part(i)[0]);
+    for (int i = threadIdx.x; i < parts; i += 128) m = fmaxf(m, part(i)[0]);
     for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0) m_s[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
     float sum = 0.0f, o[D / 32];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
+    for (int i0 = warp; i0 < parts; i0 += 128) {
         // a part without keys may hold no O: its weight 0 also says not to read it
         float w = 0.0f;
-        if (i0 + lane < parts) {
-            const float2 ml = *reinterpret_cast<const float2 *>(part(i0 + lane));
+        const int mine = i0 + lane * 4;
+        if (mine < parts) {
+            const float2 ml = *reinterpret_cast<const float2 *>(part(mine));
             w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
             sum = fmaf(w, ml.y, sum);
         }
-        const int n = min(parts - i0, 32);
-#pragma unroll 4
+        const int n = min((parts - i0 + 3) / 4, 32);
+#pragma unroll 8
         for (int i = 0; i < n; ++i) {
             const float wi = __shfl_sync(0xffffffffu, w, i);
             if (wi == 0.0f) continue;
-            const float *a = part(i0 + i) + 2 + lane * 2;
+            const float *a = part(i0 + 4 * i) + 2 + lane * 2;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 const float2 v = *reinterpret_cast<const float2 *>(a + c * 64);
@@ -953,13 +959,20 @@ __global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p) {
         }
     }
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) sum_s[warp] = sum;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        o_s[warp][c * 64 + lane * 2] = o[2 * c];
+        o_s[warp][c * 64 + lane * 2 + 1] = o[2 * c + 1];
+    }
+    __syncthreads();
+    sum = ((sum_s[0] + sum_s[1]) + sum_s[2]) + sum_s[3];
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const int token = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(token) * p.Hq);
     T *to = static_cast<T *>(p.o) + token * p.ldo + static_cast<int64_t>(head) * D;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-        *reinterpret_cast<uint32_t *>(to + c * 64 + lane * 2) = pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
+    const int c = threadIdx.x;
+    if (c < D) to[c] = from_f32<T>((((o_s[0][c] + o_s[1][c]) + o_s[2][c]) + o_s[3][c]) * inv);
+    if (c == 0 && p.lse != nullptr)
         p.lse[static_cast<int64_t>(head) * p.Nq + token] =
             sum > 0.0f ? (m + (log2f(sum) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
 }

@@ -286,6 +286,7 @@ struct CrossPlanHost {
     bool split;
     int64_t slots;            // bound on the items with it
     int32_t slot_rows;        // of one of an item's two tiles
+    int64_t rows;             // (token, query head) pairs at most
 };
 
 // A tile takes the whole group of query heads of a key head where the group
@@ -302,12 +303,13 @@ CrossPlanHost cross_plan(int64_t Nq, int32_t Hq, int32_t Hk, int32_t nseg, int32
     c.split = c.items < h3::kCrossItems && max_k > 128;
     c.slots = c.split ? c.items + h3::kCrossItems : 0;
     c.slot_rows = std::min(c.tokens, max_q) * c.hp;
+    c.rows = std::min<int64_t>(Nq, static_cast<int64_t>(nseg) * max_q) * Hq;
     return c;
 }
 
 // Behind the status block: where each row's parts are, then the parts.
-size_t cross_rows_bytes(const CrossPlanHost &c, int64_t Nq, int32_t Hq) {
-    return c.split ? h3host::round_up(static_cast<size_t>(Nq) * Hq * 8, 256) : 0;
+size_t cross_rows_bytes(const CrossPlanHost &c) {
+    return c.split ? h3host::round_up(static_cast<size_t>(c.rows) * 8, 256) : 0;
 }
 
 // TMA map over a [N, H, D] tensor of 16-bit elements, token stride ld, box
@@ -329,13 +331,13 @@ h3_status make_heads_map(CUtensorMap *map, const void *base, int64_t N, int32_t 
 }
 
 template <typename T, int D>
-h3_status launch_cross(const h3::CrossParams &p, int grid, const CUtensorMap &tq,
+h3_status launch_cross(const h3::CrossParams &p, int grid, int64_t rows, const CUtensorMap &tq,
                        const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
     using C = h3::CrossCfg<D>;
     h3::cross_attn_kernel<T, D><<<grid, C::THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
     if (p.split) {
-        const int64_t rows = static_cast<int64_t>(p.Nq) * p.Hq;   // a warp each
-        h3::cross_join_kernel<T, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
+        // a block a row: fewer than 296 items of at most 256 rows each
+        h3::cross_join_kernel<T, D><<<static_cast<unsigned>(rows), 128, 0, st>>>(p);
     }
     return launched();
 }
@@ -478,7 +480,7 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
     if (!cross_sizes_ok(Nq, 0, Hq, Hk, nseg) || (D != 64 && D != 128) || max_q < 0 || max_k < 0)
         return 0;
     const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
-    return kStatusBytes + cross_rows_bytes(c, Nq, Hq) +
+    return kStatusBytes + cross_rows_bytes(c) +
            static_cast<size_t>(c.slots) * 2 * c.slot_rows * (D + 2) * 4;
 }
 
@@ -535,7 +537,7 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     // that a masked score of -infinity stays one
     p.scale_log2 = std::max(softmax_scale * 1.4426950408889634f, 1e-30f);
     p.rows = reinterpret_cast<int2 *>(ws + kStatusBytes);
-    p.parts = reinterpret_cast<float *>(ws + kStatusBytes + cross_rows_bytes(c, Nq, Hq));
+    p.parts = reinterpret_cast<float *>(ws + kStatusBytes + cross_rows_bytes(c));
     p.slot_rows = c.slot_rows;
     CUtensorMap tq, tk, tv;
     if ((st = make_heads_map(&tq, q, Nq, Hq, D, ldq, c.hp, c.tokens)) != H3_OK) return st;
@@ -546,10 +548,10 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
                      : make_heads_map(&tv, q, Nq, Hq, D, ldq, 1, 128)) != H3_OK) return st;
     const int grid = static_cast<int>(std::min<int64_t>(d->sms, c.items + c.slots));
     if (dtype == H3_BF16)
-        return D == 128 ? launch_cross<__nv_bfloat16, 128>(p, grid, tq, tk, tv, cs)
-                        : launch_cross<__nv_bfloat16, 64>(p, grid, tq, tk, tv, cs);
-    return D == 128 ? launch_cross<__half, 128>(p, grid, tq, tk, tv, cs)
-                    : launch_cross<__half, 64>(p, grid, tq, tk, tv, cs);
+        return D == 128 ? launch_cross<__nv_bfloat16, 128>(p, grid, c.rows, tq, tk, tv, cs)
+                        : launch_cross<__nv_bfloat16, 64>(p, grid, c.rows, tq, tk, tv, cs);
+    return D == 128 ? launch_cross<__half, 128>(p, grid, c.rows, tq, tk, tv, cs)
+                    : launch_cross<__half, 64>(p, grid, c.rows, tq, tk, tv, cs);
 }
 
 }  // extern "C"
