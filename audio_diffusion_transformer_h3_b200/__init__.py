@@ -14,6 +14,7 @@ not load, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Sequence
@@ -559,11 +560,22 @@ def device_status_t(workspace, stream=None) -> int:
 # -------------------------------------------- layers around the attention (torch)
 
 _DTYPE_CODES: dict = {}
+_torch = None
+
+
+def _load_torch():
+    """torch, kept: an import statement in every helper costs these short calls
+    a tenth of their time."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
 
 
 def _dtype_code(dtype, fp32: bool = False) -> int:
     if not _DTYPE_CODES:
-        import torch
+        torch = _torch or _load_torch()
         _DTYPE_CODES.update({torch.bfloat16: H3_BF16, torch.float16: H3_FP16,
                              torch.float32: H3_FP32})
     code = _DTYPE_CODES.get(dtype, -1)
@@ -572,20 +584,16 @@ def _dtype_code(dtype, fp32: bool = False) -> int:
     return code
 
 
-def _same(first, **tensors):
-    """Every given tensor is on ``first``'s device; none asks for a gradient
-    (these calls are forward only, so a gradient would be lost in silence)."""
-    import torch
-    if not first.is_cuda:
-        raise ValueError("CUDA tensors are needed")
+def _same(device, *tensors):
+    """Every given tensor is on ``device``; none asks for a gradient (these
+    calls are forward only, so a gradient would be lost in silence)."""
+    torch = _torch or _load_torch()
     grad = torch.is_grad_enabled()
-    if grad and first.requires_grad:
-        raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is None:
             continue
-        if t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+        if t.device != device or device.type != "cuda":
+            raise ValueError(f"all tensors must be on one CUDA device: {t.device}, {device}")
         if grad and t.requires_grad:
             raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
 
@@ -594,10 +602,9 @@ def _on(device, stream):
     """Context in which a call on ``stream`` (None: the device's current one)
     allocates and launches: that device is current, and what the call allocates
     belongs to that stream. None if it is so already."""
-    import torch
-    here = torch.cuda.current_device() == device.index
+    torch = _torch or _load_torch()
     if stream is None:
-        return None if here else torch.cuda.device(device)
+        return None if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     if stream.device != device:
@@ -607,7 +614,7 @@ def _on(device, stream):
 
 def _current_stream(device) -> int:
     """Handle of the device's current stream, without building a stream object."""
-    import torch
+    torch = _torch or _load_torch()
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -632,7 +639,7 @@ def _rows(x, name):
 
 
 def _int32(x, name, shape=None):
-    import torch
+    torch = _torch or _load_torch()
     if x.dtype != torch.int32 or not x.is_contiguous() or (shape is not None and x.shape != shape):
         raise ValueError(f"{name} must be contiguous int32" + (f" {list(shape)}" if shape else ""))
 
@@ -658,6 +665,11 @@ def rope_qk_cfg(rot_dim: int, theta: float = 10000.0, layout: str = "interleaved
                           values["attn_factor"])
 
 
+@functools.lru_cache(maxsize=64)
+def _rope_qk_cfg(rot_dim, theta, layout, scaling) -> h3_rope_qk_cfg:
+    return rope_qk_cfg(rot_dim, theta, layout, dict(scaling))
+
+
 def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 10000.0,
               layout: str = "interleaved", scaling: Optional[dict] = None, out=None, stream=None):
     """(q, k) rotated by whole-number positions through h3_rope_qk_apply. q
@@ -665,9 +677,10 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
     token stride is free); positions int32 [N]. ``out``: (q_out, k_out), which
     may be (q, k). The gradient of q and k is this call on the outputs'
     gradients with negated positions."""
-    import torch
-    _same(q, k=k, positions=positions)
-    ctx = _on(q.device, stream)
+    torch = _torch or _load_torch()
+    device = q.device
+    _same(device, q, k, positions)
+    ctx = _on(device, stream)
     if ctx is not None:
         with ctx:
             return rope_qk_t(q, k, positions, rot_dim, theta, layout, scaling, out)
@@ -675,7 +688,8 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
     N, Hq, D = q.shape
     ldq = _heads(q, "q")
     _int32(positions, "positions", (N,))
-    cfg = rope_qk_cfg(D if rot_dim is None else rot_dim, theta, layout, scaling)
+    cfg = _rope_qk_cfg(D if rot_dim is None else rot_dim, theta, layout,
+                       tuple(scaling.items()) if scaling else ())
     Hk, ldk, kp = 0, 0, 0
     if k is not None:
         if k.dtype != q.dtype or k.dim() != 3 or k.shape[0] != N or k.shape[2] != D:
@@ -687,21 +701,21 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
         ldqo, ldko = Hq * D, Hk * D
     else:
         qo, ko = out
-        _same(q, q_out=qo, k_out=ko)
+        _same(device, qo, ko)
         if qo.shape != q.shape or qo.dtype != q.dtype or (k is None) != (ko is None) or (
                 k is not None and (ko.shape != k.shape or ko.dtype != q.dtype)):
             raise ValueError("out must have the shapes and type of (q, k)")
         ldqo, ldko = _heads(qo, "q_out"), 0 if ko is None else _heads(ko, "k_out")
     _check(h3_rope_qk_apply(q.data_ptr(), ldq, qo.data_ptr(), ldqo, kp, ldk,
                             0 if ko is None else ko.data_ptr(), ldko, positions.data_ptr(), cfg,
-                            N, Hq, Hk, D, code, _current_stream(q.device)),
+                            N, Hq, Hk, D, code, _current_stream(device)),
            "h3_rope_qk_apply")
     return qo, ko
 
 
 def linear_workspace_for(M: int, N: int, K: int, gated: bool = False, device=None):
     """Workspace of linear_t for x [M, K] and N output features."""
-    import torch
+    torch = _torch or _load_torch()
     n = h3_linear_workspace_size(M, N, K, H3_ACT_GATED if gated else 0)
     if n == 0:
         raise ValueError("sizes out of range")
@@ -713,9 +727,10 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
     """act(x w^T + bias) + residual through h3_linear_fwd. x [M, K], w [N, K],
     bf16 or fp16, rows 16-byte aligned (row strides a multiple of 8). ``gated``:
     w [2N, K], act(first half) * (second half). ``out`` may be ``residual``."""
-    import torch
-    _same(x, w=w, bias=bias, residual=residual, out=out, workspace=workspace)
-    ctx = _on(x.device, stream)
+    torch = _torch or _load_torch()
+    device = x.device
+    _same(device, x, w, bias, residual, out, workspace)
+    ctx = _on(device, stream)
     if ctx is not None:
         with ctx:
             return linear_t(x, w, bias, act, gated, residual, out, workspace)
@@ -744,12 +759,12 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
     elif out.shape != (M, N) or out.dtype != x.dtype:
         raise ValueError(f"out must be [{M}, {N}] of x's type")
     if workspace is None:
-        workspace = linear_workspace_for(M, N, K, gated, x.device)
+        workspace = linear_workspace_for(M, N, K, gated, device)
     _check(h3_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw,
                          0 if bias is None else bias.data_ptr(),
                          0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
                          _rows(out, "out"), M, N, K, a, code, workspace.data_ptr(),
-                         workspace.numel(), _current_stream(x.device)),
+                         workspace.numel(), _current_stream(device)),
            "h3_linear_fwd")
     return out
 
@@ -757,7 +772,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
 def cross_workspace_for(Nq: int, Hq: int, Hk: int, D: int, nseg: int, max_q: int, max_k: int,
                         device=None):
     """Workspace of cross_attn_fwd_t for these sizes."""
-    import torch
+    torch = _torch or _load_torch()
     n = h3_cross_workspace_size(Nq, Hq, Hk, D, nseg, max_q, max_k)
     if n == 0:
         raise ValueError("sizes out of range")
@@ -773,9 +788,10 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
     of 8; cu_q, cu_k int32 [nseg + 1]; key_mask bool or uint8 [Nk], False: no
     query attends to this key. A row without keys gets 0 (LSE -inf). Rows
     behind cu_q[-1] are not written."""
-    import torch
-    _same(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, key_mask=key_mask, out=out, workspace=workspace)
-    ctx = _on(q.device, stream)
+    torch = _torch or _load_torch()
+    device = q.device
+    _same(device, q, k, v, cu_q, cu_k, key_mask, out, workspace)
+    ctx = _on(device, stream)
     if ctx is not None:
         with ctx:
             return cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q, max_k, key_mask, softmax_scale,
@@ -796,9 +812,9 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
         out = q.new_empty((Nq, Hq, D))
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
-    lse = torch.empty((Hq, Nq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty((Hq, Nq), dtype=torch.float32) if return_lse else None
     if workspace is None:
-        workspace = cross_workspace_for(Nq, Hq, Hk, D, nseg, int(max_q), int(max_k), q.device)
+        workspace = cross_workspace_for(Nq, Hq, Hk, D, nseg, int(max_q), int(max_k), device)
     scale = (1.0 / math.sqrt(D)) if softmax_scale is None else float(softmax_scale)
     _check(h3_cross_attn_fwd(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
                              out.data_ptr(), _heads(out, "out"),
@@ -806,6 +822,6 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                              cu_k.data_ptr(), nseg, int(max_q), int(max_k),
                              0 if key_mask is None else key_mask.data_ptr(), Nq, Nk, Hq, Hk, D,
                              scale, code, workspace.data_ptr(), workspace.numel(),
-                             _current_stream(q.device)),
+                             _current_stream(device)),
            "h3_cross_attn_fwd")
     return (out, lse) if return_lse else out

@@ -249,7 +249,10 @@ __global__ void __launch_bounds__(384, 1)
     // ---- the boundaries, checked by every CTA; the work they make
     const int stride = cross_stride(p.nseg), entries = (p.nseg + stride - 1) / stride;
     int chunk = 1 << 24;   // more than any segment has: no split
-    if (tid == 0) units_s = 0;
+    if (tid == 0) {
+        reset_status(p.status);
+        units_s = 0;
+    }
     int bad = 0;
     unsigned long long units = 0;
     for (int i = tid; i <= p.nseg; i += C::THREADS) {

@@ -145,9 +145,25 @@ bool rope_freqs(const h3_rope_qk_cfg &c, double *f) {
 // f / (2 pi) turns a position, the fraction of a turn in units of 2^-64.
 uint64_t phase_of(double f) {
     const long double turns = static_cast<long double>(f) / 6.283185307179586476925286766559L;
-    const long double frac = turns - std::floor(turns);
-    const long double scaled = std::nearbyint(std::ldexp(frac, 64));
+    const long double whole = turns < 9e18L ? static_cast<long double>(static_cast<int64_t>(turns))
+                                            : std::floor(turns);
+    const long double scaled = (turns - whole) * 18446744073709551616.0L + 0.5L;
     return scaled >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(scaled);
+}
+
+// The phases of a cfg's pairs, or false for a cfg that is refused. A thread keeps
+// those of the last cfg it used: the powers cost more than the launch.
+bool rope_phases(const h3_rope_qk_cfg &c, uint64_t *phase) {
+    static thread_local h3_rope_qk_cfg last{};   // rot_dim 0: none
+    static thread_local uint64_t kept[h3::kRopeQkMaxPairs];
+    if (last.rot_dim == 0 || std::memcmp(&last, &c, sizeof(c)) != 0) {
+        double f[h3::kRopeQkMaxPairs];
+        if (!rope_freqs(c, f)) return false;
+        for (int j = 0; j < c.rot_dim / 2; ++j) kept[j] = phase_of(f[j]);
+        last = c;
+    }
+    std::memcpy(phase, kept, static_cast<size_t>(c.rot_dim / 2) * sizeof(uint64_t));
+    return true;
 }
 
 // Blocks of 256 places; the heads of few tokens are split so that the SMs have
@@ -359,8 +375,8 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
     if (cfg == nullptr || N < 0 || Hq < 1 || Hq > 65535 || Hk < 0 || Hk > 65535)
         return H3_ERR_INVALID_ARG;
     if (D < 2 || D > 512 || dtype < H3_BF16 || dtype > H3_FP32) return H3_ERR_UNSUPPORTED;
-    double f[h3::kRopeQkMaxPairs];
-    if (!rope_freqs(*cfg, f) || cfg->rot_dim > D) return H3_ERR_INVALID_ARG;
+    h3::RopeQkParams p;
+    if (!rope_phases(*cfg, p.phase) || cfg->rot_dim > D) return H3_ERR_INVALID_ARG;
     const int64_t wq = static_cast<int64_t>(Hq) * D, wk = static_cast<int64_t>(Hk) * D;
     if (ldq < wq || ldq_out < wq || (Hk > 0 && (ldk < wk || ldk_out < wk)))
         return H3_ERR_INVALID_ARG;
@@ -380,7 +396,6 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
     const Device *d = nullptr;
     h3_status st = device_info(&d);
     if (st != H3_OK) return st;
-    h3::RopeQkParams p;
     p.q = q; p.qo = q_out; p.ldq = ldq; p.ldqo = ldq_out;
     p.k = k; p.ko = k_out; p.ldk = ldk; p.ldko = ldk_out;
     p.positions = positions;
@@ -390,8 +405,6 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
     // channels behind the rotated part are in place already where q and k are
     p.copy = q != q_out || (Hk > 0 && k != k_out);
     p.attn_factor = static_cast<float>(cfg->attn_factor);
-    for (int j = 0; j < h3::kRopeQkMaxPairs; ++j)
-        p.phase[j] = j < cfg->rot_dim / 2 ? phase_of(f[j]) : 0;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == H3_BF16) launch_rope_qk<__nv_bfloat16>(p, half, d->sms, cs);
     else if (dtype == H3_FP16) launch_rope_qk<__half>(p, half, d->sms, cs);
@@ -435,9 +448,13 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool gated = (act & H3_ACT_GATED) != 0, skinny = M <= kSkinnyRows;
     const bool split = M > 0 && skinny && skinny_splits(N, K) > 1;
-    const cudaError_t e = cudaMemsetAsync(
-        ws, 0, split ? kStatusBytes + skinny_counter_bytes(N) : sizeof(int), cs);
-    if (e != cudaSuccess) return cuda_fail(e);
+    // the kernel's first block resets the status word; the counters of a split sum
+    // have to be zero before any block starts
+    if (M == 0 || split) {
+        const cudaError_t e = cudaMemsetAsync(
+            ws, 0, split ? kStatusBytes + skinny_counter_bytes(N) : sizeof(int), cs);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
     if (M == 0) return H3_OK;
     h3::LinearParams p;
     std::memset(&p, 0, sizeof(p));
@@ -520,9 +537,10 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     if (!d->cross_regs_ok) return H3_ERR_UNSUPPORTED;
     const CrossPlanHost c = cross_plan(Nq, Hq, Hk, nseg, max_q, max_k);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), cs);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (Nq == 0) return H3_OK;
+    if (Nq == 0) {   // else the kernel's first block resets the status word
+        const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), cs);
+        return e == cudaSuccess ? H3_OK : cuda_fail(e);
+    }
     h3::CrossParams p;
     std::memset(&p, 0, sizeof(p));
     p.o = o; p.lse = lse; p.ldo = ldo;

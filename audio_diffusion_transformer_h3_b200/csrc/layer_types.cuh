@@ -120,6 +120,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
+// The first block starts about a second (kWaitLimitCycles) before any wait of the
+// others can give up, so its reset never covers their code.
+__device__ __forceinline__ void reset_status(int *status) {
+    if (blockIdx.x == 0) atomicExch(status, 0);
+}
+
 // A wait that gave up: the block stops, the call's status word says why.
 __device__ __forceinline__ void give_up(volatile int *abort, int *status) {
     *abort = 1;

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(192, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + LT_COUNT);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     if (tid == 0) {
+        reset_status(p.status);
         for (int s = 0; s < C::MAX_STAGES; ++s) {
             mbar_init(&bars[LT_FULL + s], 1);
             mbar_init(&bars[LT_EMPTY + s], 1);
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(192)
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_s = abort + 1;
     if (tid == 0) {
+        reset_status(p.status);
         for (int s = 0; s < C::MAX_STAGES; ++s) {
             mbar_init(&bars[LS_FULL + s], 1);
             mbar_init(&bars[LS_EMPTY + s], 1);
