@@ -73,7 +73,8 @@ struct LinearTile {
     static constexpr int MAX_STAGES = 8;
     static constexpr int RING_BYTES = 4 * (A_BYTES + MAX_BN * BK * 2);   // 192 KB
     static constexpr int OFF_BIAS = RING_BYTES;                          // 256 fp32
-    static constexpr int OFF_BAR = OFF_BIAS + MAX_BN * 4;
+    static constexpr int OFF_OUT = OFF_BIAS + MAX_BN * 4;                // 4 KB a warp
+    static constexpr int OFF_BAR = OFF_OUT + 4 * 4096;
     static constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;              // + alignment slack
     static constexpr int THREADS = 192, TMA_WARP = 4, MMA_WARP = 5;
 };
@@ -93,46 +94,94 @@ __device__ __forceinline__ void linear_tile_at(const LinearParams &p, int tile, 
     n = in_group / gm;
 }
 
-// 32 finished fp32 values of row `row`, columns [col, col + 32): residual, one
-// rounding, store.
+// 32 rows x 64 columns of 16-bit values of a warp in shared memory: row r's
+// 16-byte piece i at r * 128 + ((i ^ r % 8) * 16), so that a lane's own row and
+// four rows of 128 bytes are both free of bank conflicts.
+__device__ __forceinline__ uint32_t linear_piece(uint32_t stage, int r, int i) {
+    return stage + r * 128 + ((i ^ (r & 7)) << 4);
+}
+
+// Columns [0, width) of rows [0, rows) between `stage` and memory (g: the first
+// row's first column), by the whole warp: four rows of 16-byte pieces at a time
+// where the rows allow it, else 32 elements of a row at a time.
 template <typename T>
-__device__ __forceinline__ void linear_store32(const LinearParams &p, int row, int col,
-                                               float (&v)[32]) {
-    const T *res = static_cast<const T *>(p.residual);
-    T *y = static_cast<T *>(p.y) + row * p.ldy + col;
-    const int valid = p.N - col;
-    if (res != nullptr) {
-        res += row * p.ldr + col;
+__device__ __forceinline__ void linear_rows_out(uint32_t stage, T *g, int64_t ld, int rows, int width,
+                                                bool wide, int lane) {
+    if (wide) {
+        uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-            if (p.vec_r && c + 8 <= valid) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(res + c);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < 8; ++i) v[i] = lds128(linear_piece(stage, i * 4 + lane / 8, lane & 7));
+        const int left = width - (lane & 7) * 8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack2<T>(ww[i]);
-                    v[c + 2 * i] += f.x;
-                    v[c + 2 * i + 1] += f.y;
-                }
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + lane / 8;
+            if (r >= rows || left <= 0) continue;
+            T *at = g + r * ld + (lane & 7) * 8;
+            if (left >= 8) {
+                *reinterpret_cast<uint4 *>(at) = v[i];
             } else {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i < valid) v[c + i] += to_f32(res[c + i]);
+                for (int e = 0; e < 7; ++e)
+                    if (e < left)
+                        reinterpret_cast<uint16_t *>(at)[e] = static_cast<uint16_t>(w[e / 2] >> (e % 2 * 16));
             }
         }
+        return;
     }
+    for (int r = 0; r < rows; ++r)
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        if (p.vec_y && c + 8 <= valid) {
-            *reinterpret_cast<uint4 *>(y + c) =
-                make_uint4(pack2<T>(v[c], v[c + 1]), pack2<T>(v[c + 2], v[c + 3]),
-                           pack2<T>(v[c + 4], v[c + 5]), pack2<T>(v[c + 6], v[c + 7]));
+        for (int h = 0; h < 2; ++h) {
+            const int c = h * 32 + lane;
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(linear_piece(stage, r, c >> 3) + (c & 7) * 2));
+            if (c < width) reinterpret_cast<uint16_t *>(g + r * ld)[c] = x;
+        }
+}
+
+// The first half of reading such rows: what this lane fetches (wide rows only).
+template <typename T>
+__device__ __forceinline__ void linear_rows_fetch(uint4 (&v)[8], const T *g, int64_t ld, int rows,
+                                                  int width, int lane) {
+    const int left = width - (lane & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r >= rows || left <= 0) continue;
+        const T *at = g + r * ld + (lane & 7) * 8;
+        if (left >= 8) {
+            v[i] = *reinterpret_cast<const uint4 *>(at);
         } else {
+            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < valid) y[c + i] = from_f32<T>(v[c + i]);
+            for (int e = 0; e < 7; ++e)
+                if (e < left)
+                    w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[e]) << (e % 2 * 16);
+            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
+}
+
+// The second half: into shared memory (rows that are not wide are read here).
+template <typename T>
+__device__ __forceinline__ void linear_rows_in(uint32_t stage, const uint4 (&v)[8], const T *g,
+                                               int64_t ld, int rows, int width, bool wide, int lane) {
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sts128(linear_piece(stage, i * 4 + lane / 8, lane & 7), v[i].x, v[i].y, v[i].z, v[i].w);
+        return;
+    }
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = h * 32 + lane;
+            const uint16_t x = c < width ? reinterpret_cast<const uint16_t *>(g + r * ld)[c] : 0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(linear_piece(stage, r, c >> 3) + (c & 7) * 2), "h"(x)
+                         : "memory");
+        }
 }
 
 template <typename T, bool Gated>
@@ -252,13 +301,14 @@ __global__ void __launch_bounds__(192, 1)
     } else {
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
         const T *bias = static_cast<const T *>(p.bias);
+        const uint32_t stage = smem_u32(smem + C::OFF_OUT) + warp * 4096;
         int count = 0;
         bool ok = true;   // after a wait that gave up the warps still meet at named_sync
         for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x, ++count) {
             const int buf = count & 1;
             int mt, nt;
             linear_tile_at(p, tile, mt, nt);
-            const int row = mt * C::BM + tid, col0 = nt * out_cols;
+            const int col0 = nt * out_cols;
             named_sync(1, 128);   // the last tile's bias has been read
             for (int c = tid; c < p.bn; c += 128) {
                 const int half = Gated && c >= out_cols;
@@ -266,6 +316,17 @@ __global__ void __launch_bounds__(192, 1)
                 bias_s[c] = bias != nullptr && n < p.N ? to_f32(bias[half * p.N + n]) : 0.0f;
             }
             named_sync(1, 128);
+            // this warp's rows, 64 columns at a time: the residual comes and the result
+            // goes through shared memory, in whole lines; the next residual is on its way
+            // while these columns are at work
+            const int row0 = mt * C::BM + warp * 32, rows = min(p.M - row0, 32);
+            const int cols = rows > 0 ? min(out_cols, p.N - col0) : 0;
+            const T *res = p.residual == nullptr
+                ? nullptr : static_cast<const T *>(p.residual) + row0 * p.ldr + col0;
+            T *y = static_cast<T *>(p.y) + row0 * p.ldy + col0;
+            uint4 fetched[8];
+            if (res != nullptr && p.vec_r && cols > 0)
+                linear_rows_fetch<T>(fetched, res, p.ldr, rows, min(cols, 64), lane);
             ok = ok && __all_sync(0xffffffffu,
                                   mbar_wait(&bars[LT_ACC_FULL + buf], (count >> 1) & 1, abort));
             if (!ok) {
@@ -275,22 +336,50 @@ __global__ void __launch_bounds__(192, 1)
             tc_fence_after();
             const uint32_t acc = tmem + lane_off + static_cast<uint32_t>(buf) * 256;
 #pragma unroll 1
-            for (int c = 0; c < out_cols; c += 32) {
-                uint32_t a[32];
-                float v[32];
-                tmem_ld32(acc + c, a);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]) + bias_s[c + i];
-                activate(v, p.act);
-                if constexpr (Gated) {
-                    tmem_ld32(acc + out_cols + c, a);
+            for (int c = 0; c < cols; c += 64) {
+                const int width = min(cols - c, 64);
+                if (res != nullptr) {
+                    linear_rows_in<T>(stage, fetched, res + c, p.ldr, rows, width, p.vec_r, lane);
+                    __syncwarp();
+                    if (p.vec_r && c + 64 < cols)
+                        linear_rows_fetch<T>(fetched, res + c + 64, p.ldr, rows, min(cols - c - 64, 64), lane);
+                }
+#pragma unroll 1
+                for (int h = 0; h < 64 && h < width; h += 32) {
+                    uint32_t a[32];
+                    float v[32];
+                    tmem_ld32(acc + c + h, a);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] *= __uint_as_float(a[i]) + bias_s[out_cols + c + i];
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]) + bias_s[c + h + i];
+                    activate(v, p.act);
+                    if constexpr (Gated) {
+                        tmem_ld32(acc + out_cols + c + h, a);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] *= __uint_as_float(a[i]) + bias_s[out_cols + c + h + i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // 8 columns, this lane's row
+                        const uint32_t at = linear_piece(stage, lane, h / 8 + i);
+                        if (res != nullptr) {
+                            const uint4 w = lds128(at);
+                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 f = unpack2<T>(ww[e]);
+                                v[8 * i + 2 * e] += f.x;
+                                v[8 * i + 2 * e + 1] += f.y;
+                            }
+                        }
+                        sts128(at, pack2<T>(v[8 * i], v[8 * i + 1]), pack2<T>(v[8 * i + 2], v[8 * i + 3]),
+                               pack2<T>(v[8 * i + 4], v[8 * i + 5]), pack2<T>(v[8 * i + 6], v[8 * i + 7]));
+                    }
                 }
-                if (row < p.M && col0 + c < p.N) linear_store32<T>(p, row, col0 + c, v);
+                __syncwarp();
+                linear_rows_out<T>(stage, y + c, p.ldy, rows, width, p.vec_y, lane);
+                __syncwarp();
             }
             // accumulator reads done -> the MMA warp may overwrite it
             tc_fence_before();
