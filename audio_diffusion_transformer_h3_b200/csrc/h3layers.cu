@@ -205,36 +205,41 @@ bool linear_sizes_ok(int64_t M, int32_t N, int32_t K, int32_t act) {
            K <= (1 << 20) && a >= H3_ACT_NONE && a <= H3_ACT_SILU;
 }
 
-// Rows of x up to which the weight rows are the MMA's rows (linear_skinny_kernel).
-constexpr int64_t kSkinnyRows = 128;
-// CTAs the skinny kernel aims at: two on each of 148 SMs.
-constexpr int kSkinnyCtas = 296;
+// Rows of x up to which the weight rows are the MMA's rows (linear_skinny_kernel):
+// 128 is its widest MMA, and a gated layer's two parts of 96 columns still fit the
+// ring that they are joined in.
+int64_t skinny_rows(bool gated) { return gated ? 96 : 128; }
 
 int skinny_tiles(int32_t N) { return (N + 127) / 128; }
 
-// Parts of the sum over K: as many as fill the CTAs, of 8 steps of 64 at least
-// (a shorter part is mostly the pipeline's start).
-int skinny_splits(int32_t N, int32_t K) {
+// CTAs that share the sum over K, a cluster: those that end first, with two CTAs
+// on each SM, a step of 64 as the unit and six steps for a CTA's start and end.
+int skinny_splits(int32_t N, int32_t K, int sms) {
     const int n_k = (K + 63) / 64;
-    return std::max(1, std::min({kSkinnyCtas / skinny_tiles(N), n_k / 8, 32}));
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int s = 1; s <= 8 && n_k / s >= 4; s *= 2) {
+        const int64_t waves = (static_cast<int64_t>(skinny_tiles(N)) * s + 2 * sms - 1) / (2 * sms);
+        const int64_t cost = waves * ((n_k + s - 1) / s + 6);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
 }
 
 int skinny_cols(int64_t M) { return static_cast<int>((M + 15) / 16 * 16); }
 
-// Bytes behind the status block: arrival counters, then the parts.
-size_t skinny_counter_bytes(int32_t N) {
-    return h3host::round_up(static_cast<size_t>(skinny_tiles(N)) * 4, 256);
-}
-
 // Columns of a tile: the widest part of the work is ceil(tiles / SMs) tiles a
-// CTA, each costing its columns plus about 24 columns' worth of start and end
-// (measured between 16 and 40).
+// CTA, each costing its columns plus 80 (8320 x 7168 x 5376 with tiles of 128,
+// 192, 224 and 256 columns: 19, 13, 11 and 10 rounds of 35, 48, 53 and 57 us).
 int tile_columns(int64_t M, int32_t products, int sms, bool gated) {
     int best = 256;
     int64_t best_cost = INT64_MAX;
     for (int bn = 256; bn >= 64; bn -= gated ? 64 : 32) {   // whole chunks of 32 outputs
         const int64_t tiles = (M + 127) / 128 * ((static_cast<int64_t>(products) + bn - 1) / bn);
-        const int64_t cost = (tiles + sms - 1) / sms * (bn + 24);
+        const int64_t cost = (tiles + sms - 1) / sms * (bn + 80);
         if (cost < best_cost) {
             best_cost = cost;
             best = bn;
@@ -261,10 +266,21 @@ h3_status make_rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_
 }
 
 template <typename Kernel>
-h3_status launch_mma(Kernel kernel, int grid, int threads, int smem, const CUtensorMap &a,
+h3_status launch_mma(Kernel kernel, int grid, int cluster, int threads, int smem, const CUtensorMap &a,
                      const CUtensorMap &b, const h3::LinearParams &p, cudaStream_t st) {
-    kernel<<<grid, threads, smem, st>>>(a, b, p);
-    return launched();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+    return e == cudaSuccess ? H3_OK : cuda_fail(e);
 }
 
 template <typename T, bool Gated>
@@ -273,20 +289,20 @@ h3_status launch_linear(h3::LinearParams &p, const void *x, int64_t ldx, const v
     const int64_t w_rows = Gated ? 2 * static_cast<int64_t>(p.N) : p.N;
     CUtensorMap tx, tw;
     h3_status s;
-    if (p.M <= kSkinnyRows) {
+    if (p.splits > 0) {
         using C = h3::LinearSkinny;
         if ((s = make_rows_map(&tx, x, p.M, p.K, ldx, p.cols)) != H3_OK ||
             (s = make_rows_map(&tw, w, w_rows, p.K, ldw, C::BM)) != H3_OK)
             return s;
-        return launch_mma(h3::linear_skinny_kernel<T, Gated>, p.tiles * p.splits, C::THREADS,
-                          C::SMEM_BYTES, tx, tw, p, st);
+        return launch_mma(h3::linear_skinny_kernel<T, Gated>, skinny_tiles(p.N) * p.splits, p.splits,
+                          C::THREADS, C::SMEM_BYTES, tx, tw, p, st);
     }
     using C = h3::LinearTile;
     const int out_cols = Gated ? p.bn / 2 : p.bn;
     if ((s = make_rows_map(&tx, x, p.M, p.K, ldx, C::BM)) != H3_OK ||
         (s = make_rows_map(&tw, w, w_rows, p.K, ldw, out_cols)) != H3_OK)
         return s;
-    return launch_mma(h3::linear_tile_kernel<T, Gated>, std::min(p.n_tiles, sms), C::THREADS,
+    return launch_mma(h3::linear_tile_kernel<T, Gated>, std::min(p.n_tiles, sms), 1, C::THREADS,
                       C::SMEM_BYTES, tx, tw, p, st);
 }
 
@@ -414,11 +430,7 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
 }
 
 size_t h3_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act) {
-    if (!linear_sizes_ok(M, N, K, act)) return 0;
-    if (M > kSkinnyRows || skinny_splits(N, K) == 1) return kStatusBytes;
-    const size_t part = static_cast<size_t>(act & H3_ACT_GATED ? 2 : 1) * skinny_cols(M) * 128 * 4;
-    return kStatusBytes + skinny_counter_bytes(N) +
-           static_cast<size_t>(skinny_tiles(N)) * skinny_splits(N, K) * part;
+    return linear_sizes_ok(M, N, K, act) ? kStatusBytes : 0;
 }
 
 h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
@@ -446,17 +458,11 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
     h3_status st = device_info(&d);
     if (st != H3_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const bool gated = (act & H3_ACT_GATED) != 0, skinny = M <= kSkinnyRows;
-    const bool split = M > 0 && skinny && skinny_splits(N, K) > 1;
-    // the kernel's first block resets the status word; the counters of a split sum
-    // have to be zero before any block starts
-    if (M == 0 || split) {
-        const cudaError_t e = cudaMemsetAsync(
-            ws, 0, split ? kStatusBytes + skinny_counter_bytes(N) : sizeof(int), cs);
-        if (e != cudaSuccess) return cuda_fail(e);
+    const bool gated = (act & H3_ACT_GATED) != 0;
+    if (M == 0) {   // else the kernel's first block resets the status word
+        const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), cs);
+        return e == cudaSuccess ? H3_OK : cuda_fail(e);
     }
-    if (M == 0) return H3_OK;
     h3::LinearParams p;
     std::memset(&p, 0, sizeof(p));
     p.bias = bias; p.residual = residual; p.y = y;
@@ -465,14 +471,11 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
     p.M = static_cast<int32_t>(M); p.N = N; p.K = K; p.act = act & ~H3_ACT_GATED;
     p.vec_y = aligned(y, 16) && ldy % 8 == 0;
     p.vec_r = aligned(residual, 16) && ldr % 8 == 0;
-    if (skinny) {
+    if (M <= skinny_rows(gated)) {
         using C = h3::LinearSkinny;
         p.cols = skinny_cols(M);
-        p.tiles = skinny_tiles(N);
-        p.splits = skinny_splits(N, K);
+        p.splits = skinny_splits(N, K, d->sms);
         p.stages = std::min(C::MAX_STAGES, C::RING_BYTES / ((gated ? 2 : 1) * C::W_BYTES + p.cols * C::BK * 2));
-        p.arrived = reinterpret_cast<int *>(ws + kStatusBytes);
-        p.parts = reinterpret_cast<float *>(ws + kStatusBytes + skinny_counter_bytes(N));
     } else {
         using C = h3::LinearTile;
         const int64_t products = gated ? 2 * static_cast<int64_t>(N) : N;
@@ -484,7 +487,9 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
         const int64_t tiles = static_cast<int64_t>(p.n_row_tiles) * p.n_col_tiles;
         if (tiles > INT32_MAX - 4096) return H3_ERR_INVALID_ARG;
         p.n_tiles = static_cast<int32_t>(tiles);
-        p.group_m = 32;
+        // the x rows and w slices of a round of SMs together are fewest near
+        // sqrt(148 * 256 / 128) row tiles
+        p.group_m = 16;
     }
     if (dtype == H3_BF16)
         return gated ? launch_linear<__nv_bfloat16, true>(p, x, ldx, w, ldw, d->sms, cs)

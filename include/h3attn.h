@@ -360,8 +360,7 @@ typedef enum h3_act {
 } h3_act;
 
 /* Bytes of device workspace h3_linear_fwd needs for these sizes (`act` tells
- * whether the layer is gated): a 256-byte status block and, where few rows
- * make it split the sum over K, fp32 partial products. 0 for a bad size. */
+ * whether the layer is gated): a 256-byte status block. 0 for a bad size. */
 size_t h3_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act);
 
 /* Linear layer with bias, activation and residual in the product's epilogue:
