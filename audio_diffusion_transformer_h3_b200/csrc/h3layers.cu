@@ -231,18 +231,29 @@ int skinny_splits(int32_t N, int32_t K, int sms) {
 
 int skinny_cols(int64_t M) { return static_cast<int>((M + 15) / 16 * 16); }
 
-// Columns of a tile: the widest part of the work is ceil(tiles / SMs) tiles a
-// CTA, each costing its columns plus 80 (8320 x 7168 x 5376 with tiles of 128,
-// 192, 224 and 256 columns: 19, 13, 11 and 10 rounds of 35, 48, 53 and 57 us).
-int tile_columns(int64_t M, int32_t products, int sms, bool gated) {
-    int best = 256;
+// Output columns of a tile and the parts that the last, partial round's tiles come
+// in: the cheapest sum over the rounds, a round costing its products' columns plus
+// 80 (8320 x 7168 x 5376 with tiles of 128, 192, 224 and 256 columns: 19, 13, 11
+// and 10 rounds of 35, 48, 53 and 57 us).
+struct TileShape {
+    int out_cols, pieces;
+};
+
+TileShape tile_shape(int64_t M, int32_t N, bool gated, int sms) {
+    TileShape best{};
     int64_t best_cost = INT64_MAX;
-    for (int bn = 256; bn >= 64; bn -= gated ? 64 : 32) {   // whole chunks of 32 outputs
-        const int64_t tiles = (M + 127) / 128 * ((static_cast<int64_t>(products) + bn - 1) / bn);
-        const int64_t cost = (tiles + sms - 1) / sms * (bn + 80);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = bn;
+    const int products = gated ? 2 : 1;
+    for (int cols = 256 / products; cols >= 32; cols -= 32) {   // whole chunks of 32 outputs
+        const int64_t tiles = (M + 127) / 128 * ((static_cast<int64_t>(N) + cols - 1) / cols);
+        for (int pieces = 1; pieces <= 4; pieces *= 2) {
+            // (without a whole round, smaller tiles do the same with a deeper ring)
+            if (pieces > 1 && (cols % (32 * pieces) != 0 || tiles < sms)) break;
+            const int64_t cost = tiles / sms * (products * cols + 80) +
+                                 (tiles % sms * pieces + sms - 1) / sms * (products * cols / pieces + 80);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {cols, pieces};
+            }
         }
     }
     return best;
@@ -265,9 +276,9 @@ h3_status make_rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_
     return r == CUDA_SUCCESS ? H3_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
-template <typename Kernel>
-h3_status launch_mma(Kernel kernel, int grid, int cluster, int threads, int smem, const CUtensorMap &a,
-                     const CUtensorMap &b, const h3::LinearParams &p, cudaStream_t st) {
+template <typename Kernel, typename... Args>
+h3_status launch_mma(Kernel kernel, int grid, int cluster, int threads, int smem, cudaStream_t st,
+                     const Args &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -279,7 +290,7 @@ h3_status launch_mma(Kernel kernel, int grid, int cluster, int threads, int smem
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e == cudaSuccess ? H3_OK : cuda_fail(e);
 }
 
@@ -295,15 +306,16 @@ h3_status launch_linear(h3::LinearParams &p, const void *x, int64_t ldx, const v
             (s = make_rows_map(&tw, w, w_rows, p.K, ldw, C::BM)) != H3_OK)
             return s;
         return launch_mma(h3::linear_skinny_kernel<T, Gated>, skinny_tiles(p.N) * p.splits, p.splits,
-                          C::THREADS, C::SMEM_BYTES, tx, tw, p, st);
+                          C::THREADS, C::SMEM_BYTES, st, tx, tw, p);
     }
     using C = h3::LinearTile;
-    const int out_cols = Gated ? p.bn / 2 : p.bn;
+    CUtensorMap tw_piece;
     if ((s = make_rows_map(&tx, x, p.M, p.K, ldx, C::BM)) != H3_OK ||
-        (s = make_rows_map(&tw, w, w_rows, p.K, ldw, out_cols)) != H3_OK)
+        (s = make_rows_map(&tw, w, w_rows, p.K, ldw, p.out_cols)) != H3_OK ||
+        (s = make_rows_map(&tw_piece, w, w_rows, p.K, ldw, p.out_cols / p.pieces)) != H3_OK)
         return s;
     return launch_mma(h3::linear_tile_kernel<T, Gated>, std::min(p.n_tiles, sms), 1, C::THREADS,
-                      C::SMEM_BYTES, tx, tw, p, st);
+                      C::SMEM_BYTES, st, tx, tw, tw_piece, p);
 }
 
 // ------------------------------------------------------------ cross attention
@@ -478,15 +490,18 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
         p.stages = std::min(C::MAX_STAGES, C::RING_BYTES / ((gated ? 2 : 1) * C::W_BYTES + p.cols * C::BK * 2));
     } else {
         using C = h3::LinearTile;
-        const int64_t products = gated ? 2 * static_cast<int64_t>(N) : N;
-        p.bn = tile_columns(M, static_cast<int32_t>(products), d->sms, gated);
-        p.stages = std::min(C::MAX_STAGES, C::RING_BYTES / (C::A_BYTES + p.bn * C::BK * 2));
-        const int out_cols = gated ? p.bn / 2 : p.bn;
+        const TileShape shape = tile_shape(M, N, gated, d->sms);
+        p.out_cols = shape.out_cols;
+        p.pieces = shape.pieces;
+        p.stages = std::min(C::MAX_STAGES,
+                            C::RING_BYTES / (C::A_BYTES + (gated ? 2 : 1) * p.out_cols * C::BK * 2));
         p.n_row_tiles = static_cast<int32_t>((M + C::BM - 1) / C::BM);
-        p.n_col_tiles = (N + out_cols - 1) / out_cols;
+        p.n_col_tiles = (N + p.out_cols - 1) / p.out_cols;
         const int64_t tiles = static_cast<int64_t>(p.n_row_tiles) * p.n_col_tiles;
-        if (tiles > INT32_MAX - 4096) return H3_ERR_INVALID_ARG;
-        p.n_tiles = static_cast<int32_t>(tiles);
+        if (tiles > INT32_MAX / 8) return H3_ERR_INVALID_ARG;
+        const int rest = static_cast<int>(tiles % d->sms);
+        p.whole = static_cast<int32_t>(tiles) - rest;
+        p.n_tiles = p.whole + rest * p.pieces;
         // the x rows and w slices of a round of SMs together are fewest near
         // sqrt(148 * 256 / 128) row tiles
         p.group_m = 16;

@@ -31,7 +31,8 @@ struct LinearParams {
     int32_t M, N, K, act;     // act: h3_act without the gate
     int32_t vec_y, vec_r;     // y / residual rows allow 16-byte accesses
     // tile kernel
-    int32_t bn, stages, n_row_tiles, n_col_tiles, n_tiles, group_m;
+    int32_t out_cols, stages, n_row_tiles, n_col_tiles, n_tiles, group_m;
+    int32_t whole, pieces;    // whole tiles, then the rest of them in `pieces` parts each
     // skinny kernel
     int32_t cols, splits;     // splits: the cluster's CTAs
 };
@@ -83,15 +84,26 @@ enum : int {
     LT_FULL = 0, LT_EMPTY = 8, LT_ACC_FULL = 16, LT_ACC_EMPTY = 18, LT_DRAIN = 20, LT_COUNT = 21
 };
 
-// Tile number -> (row tile, column tile): group_m row tiles sweep the columns
-// together, so the x rows and w slices in flight stay in L2.
-__device__ __forceinline__ void linear_tile_at(const LinearParams &p, int tile, int &m, int &n) {
+struct LinearTileAt {
+    int row, col, width;   // row tile, first output column, output columns
+};
+
+// Tile number -> its place: group_m row tiles sweep the columns together, so the x
+// rows and w slices in flight stay in L2; the tiles of the last, partial round of
+// SMs come in parts.
+__device__ __forceinline__ LinearTileAt linear_tile_at(const LinearParams &p, int tile) {
+    int piece = 0, width = p.out_cols;
+    if (tile >= p.whole) {
+        const int i = tile - p.whole;
+        tile = p.whole + i / p.pieces;
+        piece = i % p.pieces;
+        width = p.out_cols / p.pieces;
+    }
     const int per_group = p.group_m * p.n_col_tiles;
     const int group = tile / per_group, first = group * p.group_m;
     const int left = p.n_row_tiles - first, gm = left < p.group_m ? left : p.group_m;
     const int in_group = tile - group * per_group;
-    m = first + in_group % gm;
-    n = in_group / gm;
+    return {first + in_group % gm, in_group / gm * p.out_cols + piece * width, width};
 }
 
 // 32 rows x 64 columns of 16-bit values of a warp in shared memory: row r's
@@ -187,14 +199,15 @@ __device__ __forceinline__ void linear_rows_in(uint32_t stage, const uint4 (&v)[
 template <typename T, bool Gated>
 __global__ void __launch_bounds__(192, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tmX,
-                       const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
+                       const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmWPiece, const LinearParams p) {
     using C = LinearTile;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_k = (p.K + C::BK - 1) / C::BK;
-    const int out_cols = Gated ? p.bn / 2 : p.bn;       // outputs a tile
-    const int b_bytes = p.bn * C::BK * 2, stage_bytes = C::A_BYTES + b_bytes;
+    constexpr int W = Gated ? 2 : 1;                    // products
+    const int stage_bytes = C::A_BYTES + W * p.out_cols * C::BK * 2;
 
     float *bias_s = reinterpret_cast<float *>(smem + C::OFF_BIAS);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -233,8 +246,9 @@ __global__ void __launch_bounds__(192, 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < p.n_tiles; tile += gridDim.x) {
-            int mt, nt;
-            linear_tile_at(p, tile, mt, nt);
+            const LinearTileAt x = linear_tile_at(p, tile);
+            const CUtensorMap *w_map = x.width == p.out_cols ? &tmW : &tmWPiece;
+            const int w_bytes = x.width * C::BK * 2;
             for (int ks = 0; ks < n_k; ++ks) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&bars[LT_EMPTY + stage], phase ^ 1, abort))) {
                     ok = false;
@@ -242,12 +256,11 @@ __global__ void __launch_bounds__(192, 1)
                 }
                 if (leader) {
                     uint8_t *a = smem + stage * stage_bytes, *b = a + C::A_BYTES;
-                    mbar_arrive_expect_tx(&bars[LT_FULL + stage], stage_bytes);
-                    tma_load_rows(a, &tmX, &bars[LT_FULL + stage], ks * C::BK, mt * C::BM);
-                    tma_load_rows(b, &tmW, &bars[LT_FULL + stage], ks * C::BK, nt * out_cols);
+                    mbar_arrive_expect_tx(&bars[LT_FULL + stage], C::A_BYTES + W * w_bytes);
+                    tma_load_rows(a, &tmX, &bars[LT_FULL + stage], ks * C::BK, x.row * C::BM);
+                    tma_load_rows(b, w_map, &bars[LT_FULL + stage], ks * C::BK, x.col);
                     if (Gated)
-                        tma_load_rows(b + b_bytes / 2, &tmW, &bars[LT_FULL + stage], ks * C::BK,
-                                      p.N + nt * out_cols);
+                        tma_load_rows(b + w_bytes, w_map, &bars[LT_FULL + stage], ks * C::BK, p.N + x.col);
                 }
                 ++issued;
                 if (++stage == p.stages) { stage = 0; phase ^= 1; }
@@ -262,8 +275,6 @@ __global__ void __launch_bounds__(192, 1)
         __syncwarp();
     } else if (warp == C::MMA_WARP) {
         const uint32_t leader = elect_one();
-        const uint32_t idesc = idesc_f32<T>(C::BM, 0, false, false) |
-                               (static_cast<uint32_t>(p.bn >> 3) << 17);
         const uint64_t d0 = sdesc_sw128(smem_u32(smem), 16, 1024);
         int stage = 0, count = 0;
         uint32_t phase = 0;
@@ -275,6 +286,8 @@ __global__ void __launch_bounds__(192, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + static_cast<uint32_t>(buf) * 256;
+            const uint32_t idesc = idesc_f32<T>(C::BM, 0, false, false) |
+                                   (static_cast<uint32_t>(W * linear_tile_at(p, tile).width >> 3) << 17);
             for (int ks = 0; ks < n_k; ++ks) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars[LT_FULL + stage], phase, abort));
                 if (!ok) break;
@@ -306,11 +319,10 @@ __global__ void __launch_bounds__(192, 1)
         bool ok = true;   // after a wait that gave up the warps still meet at named_sync
         for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x, ++count) {
             const int buf = count & 1;
-            int mt, nt;
-            linear_tile_at(p, tile, mt, nt);
-            const int col0 = nt * out_cols;
+            const LinearTileAt x = linear_tile_at(p, tile);
+            const int col0 = x.col, out_cols = x.width;
             named_sync(1, 128);   // the last tile's bias has been read
-            for (int c = tid; c < p.bn; c += 128) {
+            for (int c = tid; c < W * out_cols; c += 128) {
                 const int half = Gated && c >= out_cols;
                 const int n = col0 + c - half * out_cols;
                 bias_s[c] = bias != nullptr && n < p.N ? to_f32(bias[half * p.N + n]) : 0.0f;
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(192, 1)
             // this warp's rows, 64 columns at a time: the residual comes and the result
             // goes through shared memory, in whole lines; the next residual is on its way
             // while these columns are at work
-            const int row0 = mt * C::BM + warp * 32, rows = min(p.M - row0, 32);
+            const int row0 = x.row * C::BM + warp * 32, rows = min(p.M - row0, 32);
             const int cols = rows > 0 ? min(out_cols, p.N - col0) : 0;
             const T *res = p.residual == nullptr
                 ? nullptr : static_cast<const T *>(p.residual) + row0 * p.ldr + col0;
