@@ -341,6 +341,20 @@ def test_cross(lq, lk, Hq, Hk, D, dtype):
     _check_cross(q, k, v, cu_q, cu_k, o, lse, D ** -0.5, None, "o")
 
 
+@pytest.mark.parametrize("lq", [[1], [1, 300, 2], [400]])
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "fp16"), (128, "fp16")])
+def test_cross_single_key_is_exact(lq, D, dtype):
+    """One key has the weight 1, whatever its score: O is v, bit for bit (P and the
+    sum are the same power of two). A reference maximum other than the row's own
+    shows here."""
+    import torch
+    lk = [1] * len(lq)
+    q, k, v, cu_q, cu_k = _cross_case(lq, lk, 16, 8, D, dtype)
+    o, _ = _run_cross(q, k, v, cu_q, cu_k, lq, lk)
+    want = torch.cat([v[s].repeat_interleave(2, 0).expand(n, 16, D) for s, n in enumerate(lq)])
+    assert torch.equal(o, want)
+
+
 @pytest.mark.parametrize("lk", [40, 128, 200, 300])
 @pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "fp16")])
 def test_cross_many_items_a_cta(lk, D, dtype):
