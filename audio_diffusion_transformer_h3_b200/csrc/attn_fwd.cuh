@@ -433,10 +433,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) mq[i] = __uint_as_float(s[i]);
 #pragma unroll
-            for (int c = 8; c < 128; c += 16)
+            for (int c = 8; c < 120; c += 16)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     mq[i] = fmax3(mq[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mq[i] = fmaxf(mq[i], __uint_as_float(s[120 + i]));
             const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
                                    fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
             const float m_new = mx * sl2;
