@@ -84,8 +84,10 @@ struct CrossCfg {
     static constexpr int NBOX = D / 64;
     static constexpr int BOX_BYTES = 128 * 128;
     static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
-    static constexpr int OFF_Q = 0, OFF_K = 2 * TILE_BYTES, OFF_V = 4 * TILE_BYTES;
-    static constexpr int OFF_OUT = 6 * TILE_BYTES;            // 4 KB for each softmax warp
+    // key and value tiles in flight each (what shared memory holds; a power of 2)
+    static constexpr int STAGES = D == 64 ? 4 : 2, LOG_STAGES = D == 64 ? 2 : 1;
+    static constexpr int OFF_Q = 0, OFF_K = 2 * TILE_BYTES, OFF_V = OFF_K + STAGES * TILE_BYTES;
+    static constexpr int OFF_OUT = OFF_V + STAGES * TILE_BYTES;            // 4 KB for each softmax warp
     static constexpr int SMEM_BYTES = OFF_OUT + 8 * 4096 + 1024;   // + alignment slack
     static constexpr uint32_t COL_S = 0, COL_O = 256;   // S_t at 128 t, O_t at 256 + 128 t
     static constexpr int THREADS = 384;
@@ -95,10 +97,10 @@ struct CrossCfg {
 };
 
 enum : int {
-    CB_QFULL = 0, CB_QEMPTY = 2, CB_KFULL = 4, CB_KEMPTY = 6, CB_VFULL = 8, CB_VEMPTY = 10,
-    CB_VFIX = 12, CB_SFULL = 14, CB_P1 = 16, CB_P2 = 18, CB_OFULL = 20, CB_DRAIN = 22,
-    CB_TURN = 24,   // CB_TURN * 8 is a multiple of 64
-    CB_IFULL = 32, CB_IEMPTY = 36, CB_COUNT = 40
+    CB_QFULL = 0, CB_QEMPTY = 2, CB_KFULL = 4, CB_KEMPTY = 8, CB_VFULL = 12, CB_VEMPTY = 16,
+    CB_VFIX = 20, CB_TURN = 24,   // CB_TURN * 8 is a multiple of 64
+    CB_SFULL = 32, CB_P1 = 34, CB_P2 = 36, CB_OFULL = 38, CB_DRAIN = 40, CB_IFULL = 41,
+    CB_IEMPTY = 45, CB_COUNT = 49
 };
 
 // The plan of a launch in shared memory, from one address on: the key tiles of a
@@ -291,15 +293,17 @@ __global__ void __launch_bounds__(384, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars[CB_QFULL + s], 1);
             mbar_init(&bars[CB_QEMPTY + s], 1);
+            mbar_init(&bars[CB_SFULL + s], 1);
+            mbar_init(&bars[CB_P1 + s], 4);
+            mbar_init(&bars[CB_P2 + s], 4);
+            mbar_init(&bars[CB_OFULL + s], 1);
+        }
+        for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bars[CB_KFULL + s], 1);
             mbar_init(&bars[CB_KEMPTY + s], 2);   // one commit for each tile
             mbar_init(&bars[CB_VFULL + s], 1);
             mbar_init(&bars[CB_VEMPTY + s], 2);
             mbar_init(&bars[CB_VFIX + s], 1);
-            mbar_init(&bars[CB_SFULL + s], 1);
-            mbar_init(&bars[CB_P1 + s], 4);
-            mbar_init(&bars[CB_P2 + s], 4);
-            mbar_init(&bars[CB_OFULL + s], 1);
         }
         mbar_init(&bars[CB_DRAIN], 1);
         for (int i = 0; i < kCrossRing; ++i) {
@@ -355,6 +359,9 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_at(bar0 + (CB_IEMPTY + n % kCrossRing) * 8);
     };
+    // stage of key tile number n of this CTA, and the parity of its phase there
+    auto stage_of = [](int n) { return n & (C::STAGES - 1); };
+    auto phase_of = [](int n) { return static_cast<uint32_t>(n >> C::LOG_STAGES) & 1u; };
     // keys of key tile j
     auto keys_in = [](int k_left, int j) { return min(k_left - j * 128, 128); };
     // which of a key tile's 32 keys from `c` on count, for all lanes
@@ -399,8 +406,8 @@ __global__ void __launch_bounds__(384, 1)
             item_done(n);
             if (n_kv < 0) break;
             for (int j = 0; ok && j < n_kv; ++j) {
-                const int s = nk & 1;
-                ok = wait(CB_KEMPTY + s, ((nk >> 1) & 1) ^ 1);
+                const int s = stage_of(nk);
+                ok = wait(CB_KEMPTY + s, phase_of(nk) ^ 1);
                 if (!ok) break;
                 if (leader) {
                     mbar_arrive_expect_tx(&bars[CB_KFULL + s], C::TILE_BYTES);
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(384, 1)
                         ++nq[t];
                     }
                 if (!ok) break;
-                ok = wait(CB_VEMPTY + s, ((nv >> 1) & 1) ^ 1);
+                ok = wait(CB_VEMPTY + s, phase_of(nv) ^ 1);
                 if (!ok) break;
                 if (leader) {
                     mbar_arrive_expect_tx(&bars[CB_VFULL + s], C::TILE_BYTES);
@@ -436,10 +443,10 @@ __global__ void __launch_bounds__(384, 1)
             // the copies still in flight land before shared memory is released
             for (int t = 0; t < 2; ++t)
                 if (nq[t] > 0) mbar_wait(&bars[CB_QFULL + t], (nq[t] - 1) & 1, nullptr);
-            for (int j = max(nk - 2, 0); j < nk; ++j)
-                mbar_wait(&bars[CB_KFULL + (j & 1)], (j >> 1) & 1, nullptr);
-            for (int j = max(nv - 2, 0); j < nv; ++j)
-                mbar_wait(&bars[CB_VFULL + (j & 1)], (j >> 1) & 1, nullptr);
+            for (int j = max(nk - C::STAGES, 0); j < nk; ++j)
+                mbar_wait(&bars[CB_KFULL + stage_of(j)], phase_of(j), nullptr);
+            for (int j = max(nv - C::STAGES, 0); j < nv; ++j)
+                mbar_wait(&bars[CB_VFULL + stage_of(j)], phase_of(j), nullptr);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -454,31 +461,39 @@ __global__ void __launch_bounds__(384, 1)
             const int n_kv = lds32(x + CX_N_KV), k0 = lds32(x + CX_K0), k_left = lds32(x + CX_K_LEFT);
             item_done(n);
             if (n_kv < 0) break;
-            for (int j = 0; ok && j < n_kv; ++j, ++nv) {
-                const int keys = keys_in(k_left, j), s = nv & 1, rows = (keys + 15) / 16 * 16;
-                const bool fix = p.mask != nullptr || keys % 16 != 0;
-                uint32_t valid[4] = {0, 0, 0, 0};
-                if (fix) {
+            // the mask of a key tile is read while the tile before is at work
+            uint32_t bytes = 0;   // of keys lane, lane + 32, lane + 64, lane + 96
+            auto mask_of = [&](int j) {
+                uint32_t b = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) valid[i] = keys_valid(k0 + j * 128, keys, i * 32);
+                for (int i = 0; i < 4; ++i) {
+                    const int c = j * 128 + i * 32 + lane;
+                    if (c < k_left && (p.mask == nullptr || p.mask[k0 + c] != 0)) b |= 1u << i;
                 }
+                return b;
+            };
+            if (n_kv > 0) bytes = mask_of(0);
+            for (int j = 0; ok && j < n_kv; ++j, ++nv) {
+                const int keys = keys_in(k_left, j), s = stage_of(nv);
+                const bool fix = p.mask != nullptr || keys % 16 != 0;
+                const uint32_t now = bytes;
+                if (j + 1 < n_kv) bytes = mask_of(j + 1);
                 // every phase is waited for, those of tiles that need nothing too: a
                 // parity tells a phase from its neighbours only
-                ok = wait(CB_VFULL + s, (nv >> 1) & 1);
+                ok = wait(CB_VFULL + s, phase_of(nv));
                 if (!ok) break;
                 if (!fix) continue;
-                uint8_t *v = smem + C::OFF_V + s * C::TILE_BYTES;
+                uint8_t *v = smem + C::OFF_V + s * C::TILE_BYTES + (lane & 7) * 16;
                 // four rows a step, eight lanes a row
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    for (int r0 = 0; r0 < 32 && i * 32 + r0 < rows; r0 += 4) {
-                        if (((valid[i] >> r0) & 15u) == 15u) continue;
-                        const int r = i * 32 + r0 + lane / 8;
-                        if (!((valid[i] >> (r & 31)) & 1u))
+                    const uint32_t valid = __ballot_sync(0xffffffffu, (now >> i) & 1u) >> (lane / 8);
+#pragma unroll
+                    for (int r = 0; r < 32; r += 4)
+                        if (!((valid >> r) & 1u))
                             for (int b = 0; b < C::NBOX; ++b)
-                                *reinterpret_cast<uint4 *>(v + b * C::BOX_BYTES + r * 128 +
-                                                           (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                                *reinterpret_cast<uint4 *>(v + b * C::BOX_BYTES + (i * 32 + r + lane / 8) * 128) =
+                                    make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -538,10 +553,10 @@ __global__ void __launch_bounds__(384, 1)
                 ok = mma_wait(CB_QFULL, nq & 1);
                 nq ^= 1u;
                 for (int j = -2; ok && j < n_kv; ++j) {   // key tile j: values of j, scores of j + 2
-                    const int t = j & 1, s = nkv & 1;
+                    const int t = j & 1, s = stage_of(nkv);
                     if (j >= 0) {
                         const int keys = keys_in(k_left, j), n16 = (keys + 15) / 16;
-                        ok = mma_wait(CB_VFULL + s, (nkv >> 1) & 1);
+                        ok = mma_wait(CB_VFULL + s, phase_of(nkv));
                         if (ok && (p.mask != nullptr || keys % 16 != 0)) {
                             ok = mma_wait(CB_VFIX + s, (fixes >> s) & 1);
                             fixes ^= 1u << s;
@@ -560,33 +575,33 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     if (j + 2 < n_kv) {
                         const int at = j < 0 ? nkv + j + 2 : nkv + 1;   // = this item's key tile j + 2
-                        ok = mma_wait(CB_KFULL + (at & 1), (at >> 1) & 1);
+                        ok = mma_wait(CB_KFULL + stage_of(at), phase_of(at));
                         if (!ok) break;
-                        issue_s(t, 0, at & 1, keys_in(k_left, j + 2));
+                        issue_s(t, 0, stage_of(at), keys_in(k_left, j + 2));
                         umma_commit_w(&bars[CB_SFULL + t], leader);
-                        umma_commit_w(&bars[CB_KEMPTY + (at & 1)], leader);
-                        umma_commit_w(&bars[CB_KEMPTY + (at & 1)], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + stage_of(at)], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + stage_of(at)], leader);
                         if (j + 3 == n_kv) umma_commit_w(&bars[CB_QEMPTY], leader);
                     }
                 }
                 continue;
             }
             for (int t = 0; ok && n_kv > 0 && t < n_t; ++t) {
-                ok = mma_wait(CB_QFULL + t, (nq >> t) & 1) && mma_wait(CB_KFULL + (nkv & 1), (nkv >> 1) & 1);
+                ok = mma_wait(CB_QFULL + t, (nq >> t) & 1) && mma_wait(CB_KFULL + stage_of(nkv), phase_of(nkv));
                 if (!ok) break;
-                issue_s(t, t, nkv & 1, keys_in(k_left, 0));
+                issue_s(t, t, stage_of(nkv), keys_in(k_left, 0));
                 umma_commit_w(&bars[CB_SFULL + t], leader);
-                umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
-                if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (nkv & 1)], leader);
+                umma_commit_w(&bars[CB_KEMPTY + stage_of(nkv)], leader);
+                if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + stage_of(nkv)], leader);
                 if (n_kv == 1) umma_commit_w(&bars[CB_QEMPTY + t], leader);
                 nq ^= 1u << t;
             }
             for (int j = 0; ok && j < n_kv; ++j, ++nkv) {
                 // everything but P is waited for ahead of P, whose arrival is what the
                 // tensor cores wait for
-                const int s = nkv & 1, keys = keys_in(k_left, j), n16 = (keys + 15) / 16;
+                const int s = stage_of(nkv), s1 = stage_of(nkv + 1), keys = keys_in(k_left, j), n16 = (keys + 15) / 16;
                 const bool more = j + 1 < n_kv;
-                ok = mma_wait(CB_VFULL + s, (nkv >> 1) & 1);
+                ok = mma_wait(CB_VFULL + s, phase_of(nkv));
                 if (ok && (p.mask != nullptr || keys % 16 != 0)) {
                     ok = mma_wait(CB_VFIX + s, (fixes >> s) & 1);
                     fixes ^= 1u << s;
@@ -596,16 +611,16 @@ __global__ void __launch_bounds__(384, 1)
                     ok = mma_wait(CB_P1 + t, (g >> t) & 1);
                     if (!ok) break;
                     issue_pv(t, s, 0, n16, j > 0);
-                    if (more && t == 0) ok = mma_wait(CB_KFULL + (s ^ 1), ((nkv + 1) >> 1) & 1);
+                    if (more && t == 0) ok = mma_wait(CB_KFULL + s1, phase_of(nkv + 1));
                     ok = ok && mma_wait(CB_P2 + t, (g >> t) & 1);
                     if (!ok) break;
                     issue_pv(t, s, 4, n16, true);
                     if (more) {
                         umma_commit_w(&bars[CB_VEMPTY + s], leader);
-                        issue_s(t, t, s ^ 1, next_keys);
+                        issue_s(t, t, s1, next_keys);
                         umma_commit_w(&bars[CB_SFULL + t], leader);
-                        umma_commit_w(&bars[CB_KEMPTY + (s ^ 1)], leader);
-                        if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + (s ^ 1)], leader);
+                        umma_commit_w(&bars[CB_KEMPTY + s1], leader);
+                        if (n_t == 1) umma_commit_w(&bars[CB_KEMPTY + s1], leader);
                         if (j + 2 == n_kv) umma_commit_w(&bars[CB_QEMPTY + t], leader);
                     } else {
                         umma_commit_w(&bars[CB_OFULL + t], leader);

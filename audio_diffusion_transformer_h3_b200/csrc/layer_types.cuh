@@ -57,14 +57,6 @@ __device__ __forceinline__ void tma_load_rows(void *smem_dst, const CUtensorMap 
         : "memory");
 }
 
-// The same 3-D tile's lines to L2 only.
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t c0, int32_t c1,
-                                                int32_t c2) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-
 // Barrier among `threads` threads of the block (ids 1..15).
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
