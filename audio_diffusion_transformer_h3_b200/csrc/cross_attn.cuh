@@ -352,8 +352,12 @@ __global__ void __launch_bounds__(384, 1)
         return __all_sync(0xffffffffu, mbar_wait_at(bar0 + bar * 8, parity, abort_at));
     };
     // The n-th item: its ring slot, when it is there, and its release by this warp.
+    // (These waits last as long as items do, so their limit is that of many tiles' waits;
+    // a wait that gives up elsewhere in the CTA ends them at once.)
+    constexpr long long kItemLimit = 64 * kWaitLimitCycles;
     auto item_wait = [&](uint32_t n) {
-        return wait(CB_IFULL + n % kCrossRing, (n / kCrossRing) & 1);
+        return __all_sync(0xffffffffu, mbar_wait_at(bar0 + (CB_IFULL + n % kCrossRing) * 8,
+                                                    (n / kCrossRing) & 1, abort_at, kItemLimit));
     };
     auto item_done = [&](uint32_t n) {
         __syncwarp();
@@ -377,7 +381,8 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = true;
         for (int it = blockIdx.x; ok; it += gridDim.x, ++n) {
             const bool more = it < lds32(plan + CP_TOTAL);
-            ok = wait(CB_IEMPTY + n % kCrossRing, ((n / kCrossRing) & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, mbar_wait_at(bar0 + (CB_IEMPTY + n % kCrossRing) * 8,
+                                                      ((n / kCrossRing) & 1) ^ 1, abort_at, kItemLimit));
             if (!ok) break;
             if (lane == 0) {
                 const uint32_t to = ring + (n % kCrossRing) * CX_BYTES;

@@ -291,6 +291,7 @@ h3_status launch_mma(Kernel kernel, int grid, int cluster, int threads, int smem
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();   // not to be found by the next call
     return e == cudaSuccess ? H3_OK : cuda_fail(e);
 }
 
@@ -532,7 +533,8 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     if (!cross_sizes_ok(Nq, Nk, Hq, Hk, nseg)) return H3_ERR_INVALID_ARG;
     if ((D != 64 && D != 128) || (dtype != H3_BF16 && dtype != H3_FP16))
         return H3_ERR_UNSUPPORTED;
-    if (!std::isfinite(softmax_scale) || softmax_scale < 0.0f) return H3_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale * 1.4426950408889634f) || softmax_scale < 0.0f)
+        return H3_ERR_INVALID_ARG;
     if (cu_q == nullptr || cu_k == nullptr) return H3_ERR_INVALID_ARG;
     if (Nq > 0 && (q == nullptr || o == nullptr || max_q < 1 || max_q > Nq))
         return H3_ERR_INVALID_ARG;

@@ -64,7 +64,8 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 
 // mbar_wait, mbar_arrive and give_up with shared-memory addresses, for code that is
 // short of registers.
-__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, uint32_t abort) {
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, uint32_t abort,
+                                             long long limit_cycles = kWaitLimitCycles) {
     auto done = [&]() {
         uint32_t ok;
         asm volatile(
@@ -80,7 +81,7 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, uint
         if (done()) return true;
         int stop;
         asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
-        if (stop != 0 || clock64() - t0 > kWaitLimitCycles) return false;
+        if (stop != 0 || clock64() - t0 > limit_cycles) return false;
     }
 }
 

@@ -337,8 +337,8 @@ h3_status h3_rope_qk_freqs(const h3_rope_qk_cfg *cfg, double *freqs);
  *              k and k_out NULL and Hk = 0: q alone.
  *   positions: device int32 [N], any value. Angles are exact to 2^-33 turns
  *              at every position (fixed-point phase), cos and sin fp32.
- *   N >= 0 (0 is a no-op), 1 <= Hq <= 65535, 0 <= Hk <= 65535, 2 <= D <= 512,
- *   N * ld < 2^47, dtype H3_BF16, H3_FP16 or H3_FP32; pointers aligned to
+ *   0 <= N <= 2^30 (0 is a no-op), 1 <= Hq <= 65535, 0 <= Hk <= 65535,
+ *   2 <= D <= 512, N * ld < 2^47, dtype H3_BF16, H3_FP16 or H3_FP32; pointers aligned to
  *   their element (16-byte aligned rows and halves take the vector path).
  * Rounded once to dtype. The gradient with respect to q and k is the same
  * call on the outputs' gradients with negated positions. Deterministic; one
@@ -384,7 +384,9 @@ size_t h3_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act);
  *              not shared by calls that run concurrently.
  * fp32 accumulation, bias, activation and residual in fp32, one rounding.
  * Deterministic (also where the sum over K is split: the parts are added in
- * their order). */
+ * their order). One kernel launch. What the device finds (a bounded wait that
+ * gave up) stands in the workspace's status word (h3_read_device_status), which
+ * every call resets. */
 h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
                         const void *bias, const void *residual, int64_t ldr, void *y,
                         int64_t ldy, int64_t M, int32_t N, int32_t K, int32_t act,
@@ -392,8 +394,8 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
                         h3_stream_t stream);
 
 /* Bytes of device workspace h3_cross_attn_fwd needs: a 256-byte status block
- * and, where few query rows make it split the keys, fp32 partial results.
- * 0 for a bad size. */
+ * and, where few query rows make it split the keys, 8 bytes a row and fp32
+ * partial results (at most 592 x 256 rows of D + 2 values). 0 for a bad size. */
 size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, int32_t nseg,
                                int32_t max_q, int32_t max_k);
 
@@ -419,11 +421,13 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
  *              What k and v hold at such keys has no influence, whatever it is.
  *   Nq, Nk   : 0 <= Nq, Nk < 2^31 (Nq = 0 is a no-op); 1 <= Hk <= Hq <= 65535,
  *              Hq a multiple of Hk; D in {64, 128}; 1 <= nseg <= 65535;
- *              softmax_scale finite, >= 0; dtype H3_BF16 or H3_FP16.
+ *              softmax_scale finite (times log2 e too), >= 0; dtype H3_BF16 or H3_FP16.
  *   workspace: device, 256-byte aligned, >= h3_cross_workspace_size bytes; not
  *              shared by calls that run concurrently.
  * fp32 scores, sums and accumulation; P is rounded to dtype before the PV
- * product. Deterministic, the split over keys included. */
+ * product. Deterministic, the split over keys included. Launches: the attention
+ * kernel and, where it splits the keys, one that joins the parts. The status word
+ * is reset by every call. */
 h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk,
                             const void *v, int64_t ldv, void *o, int64_t ldo, float *lse,
                             const int32_t *cu_q, const int32_t *cu_k, int32_t nseg,

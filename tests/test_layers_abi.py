@@ -54,7 +54,7 @@ def test_rope_refusals():
         assert _rope(_cfg(**bad)) == h3.H3_ERR_INVALID_ARG, bad
     for bad in (dict(N=-1), dict(Hq=0), dict(Hq=65536), dict(Hk=-1), dict(ldq=1023),
                 dict(ldk_out=255), dict(q=0), dict(k=0), dict(k_out=0), dict(positions=0),
-                dict(ldq=1 << 46), dict(q_out=0x10000, ldq_out=1032)):
+                dict(ldq=1 << 46), dict(N=(1 << 30) + 1), dict(q_out=0x10000, ldq_out=1032)):
         assert _rope(**bad) == h3.H3_ERR_INVALID_ARG, bad
     for bad in (dict(D=513), dict(D=1), dict(dtype=3), dict(dtype=-1)):
         assert _rope(**bad) == h3.H3_ERR_UNSUPPORTED, bad
@@ -118,7 +118,7 @@ def test_cross_refusals():
                 dict(Hq=65536), dict(Hq=1), dict(nseg=0), dict(nseg=65536), dict(max_q=0),
                 dict(max_q=101), dict(max_k=-1), dict(max_k=71), dict(q=0), dict(o=0), dict(k=0),
                 dict(v=0), dict(cu_q=0), dict(cu_k=0), dict(softmax_scale=math.inf),
-                dict(softmax_scale=-1.0), dict(ldq=504), dict(ldv=248), dict(ldo=504),
+                dict(softmax_scale=-1.0), dict(softmax_scale=3e38), dict(ldq=504), dict(ldv=248), dict(ldo=504),
                 dict(o=0x10000), dict(o=0x30000), dict(ldk=1 << 32)):
         assert _cross(**bad) == h3.H3_ERR_INVALID_ARG, bad
     for bad in (dict(D=96), dict(dtype=2), dict(dtype=-1)):

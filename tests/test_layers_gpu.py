@@ -596,6 +596,47 @@ def test_block_on_another_stream_and_captured():
         assert torch.equal(got, _block(h3, t))
 
 
+def test_short_calls_captured_and_replayed():
+    """One graph with the forms for few rows: the sum over K shared by a cluster,
+    the keys split and joined, one token rotated; replayed on changed inputs."""
+    import torch
+    h3 = _h3()
+    x, w, b, _ = _linear_case(3, 512, 4096, "silu", False, True, False, "bf16")
+    q0, k, v, cu_q, cu_k = _cross_case([1, 2], [5000, 300], 8, 2, 64, "bf16")
+    pos = torch.tensor([7, 100000, -5], dtype=torch.int32, device="cuda")
+
+    def run():
+        y = h3.linear_t(x, w, b, "silu")
+        q, _ = h3.rope_qk_t(y.view(3, 8, 64), None, pos, layout="half")
+        return h3.cross_attn_fwd_t(q, k, v, cu_q, cu_k, 2, 5000, return_lse=True)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for factor in (1.0, 0.5, -2.0):
+        x.mul_(factor)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_same_buffer_twice():
+    """One tensor as several inputs: keys as values, the input as the residual, q as k."""
+    import torch
+    h3 = _h3()
+    q, k, _, cu_q, cu_k = _cross_case([70, 1], [200, 900], 4, 2, 64, "bf16")
+    o, lse = _run_cross(q, k, k, cu_q, cu_k, [70, 1], [200, 900])
+    _check_cross(q, k, k, cu_q, cu_k, o, lse, 0.125, None, "k as v")
+    x, w, b, _ = _linear_case(150, 256, 256, "none", False, True, False, "bf16")
+    _check_linear(x, w, b, "none", False, x, h3.linear_t(x, w, b, residual=x), "x as residual")
+    pos = torch.arange(71, dtype=torch.int32, device="cuda")
+    a, c = h3.rope_qk_t(q, q, pos)
+    assert torch.equal(a, c)
+
+
 def test_two_calls_at_once():
     """Calls on two streams with workspaces of their own do not disturb each other."""
     import torch
