@@ -503,9 +503,11 @@ h3_status h3_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
         const int rest = static_cast<int>(tiles % d->sms);
         p.whole = static_cast<int32_t>(tiles) - rest;
         p.n_tiles = p.whole + rest * p.pieces;
-        // the x rows and w slices of a round of SMs together are fewest near
-        // sqrt(148 * 256 / 128) row tiles
-        p.group_m = 16;
+        // the x rows and w slices that a round of SMs reads are fewest near
+        // sqrt(148 * 256 / 128) = 17 row tiles together; 8320 x 7168 x 5376 and the
+        // gated 8320 x 5376 x 14336 took 550 and 2021 us with 12, 546 and 1988 with
+        // 16, 546 and 1977 with 20, 555 and 1965 with 32
+        p.group_m = 20;
     }
     if (dtype == H3_BF16)
         return gated ? launch_linear<__nv_bfloat16, true>(p, x, ldx, w, ldw, d->sms, cs)

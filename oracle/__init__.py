@@ -27,6 +27,8 @@ What it computes, and the passages it follows:
 * ``sage``        -- the lossy SAGE-style FP8 attention: e4m3 Q/K with
   per-token and per-16-key scales, FP8 P and V ("MiniMax H3" vLLM-Omni
   recipe, section "Attention Backends"), with its e4m3 codec.
+* ``layers``      -- float64 references of the layers around the attention:
+  1-D rotary positions, linear layer with epilogue, cross attention.
 
 Readings where the pages say nothing (pair layout, frequency schedule,
 audio-token clock, reference layout) are listed in the design notes of the
