@@ -3,16 +3,19 @@
 //
 // Two kernels, both fed by TMA through a ring of 64-wide K steps, multiplied
 // by tcgen05.mma into fp32 TMEM accumulators, every wait bounded:
-//   linear_tile_kernel  rows of x are the 128 rows of the MMA, BN weight rows
+//   linear_tile_kernel  rows of x are the 128 rows of the MMA, 32 to 256 weight rows
 //       its columns. Persistent, two accumulators, so that a tile's epilogue
-//       runs under the next tile's main loop. Bound by the tensor cores.
+//       runs under the next tile's main loop. Bound by the tensor cores: 71 % of
+//       their cycles in a single launch of 4160 x 7168 x 5376 (239 us), 1170 to
+//       1300 TFLOP/s in a loop under the power cap (8320 rows).
 //   linear_skinny_kernel  few rows of x: weight rows are the MMA's 128 rows
 //       and x its 16..128 columns, so nothing of the MMA is spent on absent
 //       rows. Bound by reading w once; to have all SMs read, the sum over K
 //       is split over a cluster of up to 8 CTAs, which then share out the
 //       columns: each adds the parts of its own, read from the others' shared
 //       memory in their order (parts joined through global memory by the last
-//       CTA took 45 us instead of 17 for 32 rows of 7168 x 5376).
+//       CTA took 45 us instead of 22 for 32 rows of 7168 x 5376). Measured: two
+//       rows of 5376 x 32256 at 6.1 TB/s, 94 % of a plain copy's rate.
 // A gated layer keeps the gate and the up product of the same outputs side by
 // side in TMEM and multiplies them in the epilogue.
 #pragma once
