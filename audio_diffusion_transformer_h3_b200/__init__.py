@@ -618,6 +618,11 @@ def _current_stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _like(x):
+    """A contiguous tensor of x's shape and type."""
+    return _torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _heads(x, name):
     """(token stride) of a [N, H, D] tensor whose heads are contiguous."""
     if x.dim() != 3:
@@ -696,8 +701,7 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
             raise ValueError("k must be [N, Hk, D] of q's type")
         Hk, ldk, kp = k.shape[1], _heads(k, "k"), k.data_ptr()
     if out is None:
-        qo = q.new_empty((N, Hq, D))
-        ko = None if k is None else q.new_empty((N, Hk, D))
+        qo, ko = _like(q), None if k is None else _like(k)
         ldqo, ldko = Hq * D, Hk * D
     else:
         qo, ko = out
@@ -809,7 +813,7 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                                  key_mask.dtype not in (torch.bool, torch.uint8)):
         raise ValueError(f"key_mask must be contiguous bool or uint8 [{Nk}]")
     if out is None:
-        out = q.new_empty((Nq, Hq, D))
+        out = _like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
     lse = q.new_empty((Hq, Nq), dtype=torch.float32) if return_lse else None

@@ -637,6 +637,38 @@ def test_same_buffer_twice():
     assert torch.equal(a, c)
 
 
+def test_offsets_beyond_32_bits():
+    """Rows that begin more than 2^31 elements into their tensor (5 GB views of one
+    buffer): the last ones are right."""
+    import torch
+    h3 = _h3()
+    rows, ld, tail = 150000, 16384, 300
+    wide = torch.zeros(rows, ld, dtype=torch.bfloat16, device="cuda")
+    assert (rows - tail) * ld > 2 ** 31
+    wide[-tail:, :1024] = _draw(np.random.default_rng(9), (tail, 1024), torch.bfloat16)
+    # rotary: q and k read and written in place of the wide rows' first 384 channels
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    q, k = wide[:, :256].view(rows, 4, 64), wide[:, 256:384].view(rows, 2, 64)
+    want = h3.rope_qk_t(q[-tail:].contiguous(), k[-tail:].contiguous(), pos[-tail:])
+    h3.rope_qk_t(q, k, pos, out=(q, k))
+    assert torch.equal(q[-tail:], want[0]) and torch.equal(k[-tail:], want[1])
+    # linear: x, residual and y in the wide rows
+    w = _draw(np.random.default_rng(10), (96, 256), torch.bfloat16, 1 / 16)
+    x, r, y = wide[:, :256], wide[:, 256:352], wide[:, 2048:2144]
+    h3.linear_t(x, w, residual=r, out=y)
+    _check_linear(x[-tail:], w, None, "none", False, r[-tail:], y[-tail:], "linear")
+    # cross attention: the second of two segments, queries and keys at the end
+    cu_q = torch.tensor([0, 10, 10 + tail], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, rows - tail, rows], dtype=torch.int32, device="cuda")
+    v, qq = wide[:, 512:640].view(rows, 2, 64), q[-tail - 10:]
+    mask = torch.ones(rows, dtype=torch.bool, device="cuda")
+    mask[-1] = False
+    o, lse = h3.cross_attn_fwd_t(qq, k, v, cu_q, cu, tail, rows, key_mask=mask, return_lse=True)
+    near = torch.tensor([0, tail], dtype=torch.int32, device="cuda")
+    _check_cross(qq[10:], k[-tail:], v[-tail:], near, near, o[10:], lse[:, 10:], 0.125, mask[-tail:],
+                 "cross")
+
+
 def test_two_calls_at_once():
     """Calls on two streams with workspaces of their own do not disturb each other."""
     import torch
