@@ -196,42 +196,6 @@ __device__ __forceinline__ void fmul2(float &y0, float &y1, float x0, float x1, 
         : "=f"(y0), "=f"(y1) : "f"(x0), "f"(x1), "l"(s));
 }
 
-// 2^x for two lanes on the FMA and integer pipes: x = j + f with j = rint(x)
-// and |f| <= 1/2, 2^f as a polynomial of degree 4 fitted for the least maximum
-// relative error on [-1/2, 1/2] (2.6e-6, below every rounding of P and small
-// enough for the fp32 row sums), times 2^j by the exponent field. x below -126
-// counts as -126.
-__device__ __forceinline__ void cross_exp2_fma2(float &y0, float &y1, float x0, float x1) {
-    x0 = fmaxf(x0, -126.0f);
-    x1 = fmaxf(x1, -126.0f);
-    uint32_t t0, t1, p0, p1;
-    asm("{\n\t.reg .b64 xa, ta, ra, fa, pa, sh, nsh, nm1, c0, c1, c2, c3, c4;\n\t"
-        "mov.b64 xa, {%4, %5};\n\t"
-        "mov.b64 sh, {%6, %6};\n\t"
-        "mov.b64 nsh, {%7, %7};\n\t"
-        "mov.b64 nm1, {%8, %8};\n\t"
-        "mov.b64 c0, {%9, %9};\n\t"
-        "mov.b64 c1, {%10, %10};\n\t"
-        "mov.b64 c2, {%11, %11};\n\t"
-        "mov.b64 c3, {%12, %12};\n\t"
-        "mov.b64 c4, {%13, %13};\n\t"
-        "add.rn.f32x2 ta, xa, sh;\n\t"
-        "add.rn.f32x2 ra, ta, nsh;\n\t"
-        "fma.rn.f32x2 fa, ra, nm1, xa;\n\t"
-        "fma.rn.f32x2 pa, c4, fa, c3;\n\t"
-        "fma.rn.f32x2 pa, pa, fa, c2;\n\t"
-        "fma.rn.f32x2 pa, pa, fa, c1;\n\t"
-        "fma.rn.f32x2 pa, pa, fa, c0;\n\t"
-        "mov.b64 {%0, %1}, ta;\n\t"
-        "mov.b64 {%2, %3}, pa;\n\t}"
-        : "=r"(t0), "=r"(t1), "=r"(p0), "=r"(p1)
-        : "f"(x0), "f"(x1), "f"(12582912.0f), "f"(-12582912.0f), "f"(-1.0f),
-          "f"(0.9999992847442627f), "f"(0.6931217908859253f), "f"(0.240247443318367f),
-          "f"(0.05591786280274391f), "f"(0.009570102207362652f));
-    y0 = __uint_as_float(t0 * 8388608u + p0);
-    y1 = __uint_as_float(t1 * 8388608u + p1);
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(384, 1)
     cross_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -778,7 +742,9 @@ __global__ void __launch_bounds__(384, 1)
                 const float nm = P_SHIFT - m;
                 uint64_t acc0 = 0, acc1 = 0;
                 const uint64_t s2 = f2_splat(sl2), n2 = f2_splat(nm);
-                // P of keys [32 h, 32 h + 32), three pairs of eight on the FMA pipe
+                // P of keys [32 h, 32 h + 32). All exponentials on MUFU: with three pairs of
+                // eight as polynomials on the FMA pipe, as the dense kernel has them, the
+                // packed clips took 2 % longer (items too short for a steady alternation)
                 auto exp_part = [&](const int h) {
                     uint32_t pk[16];
 #pragma unroll
@@ -786,12 +752,8 @@ __global__ void __launch_bounds__(384, 1)
                         float x0, x1, p0, p1;
                         ffma2(x0, x1, __uint_as_float(s[32 * h + 2 * c]),
                               __uint_as_float(s[32 * h + 2 * c + 1]), s2, n2);
-                        if ((c & 7) >= 5) {
-                            cross_exp2_fma2(p0, p1, x0, x1);
-                        } else {
-                            p0 = ex2_approx(x0);
-                            p1 = ex2_approx(x1);
-                        }
+                        p0 = ex2_approx(x0);
+                        p1 = ex2_approx(x1);
                         if (c & 1) fadd2(acc1, p0, p1); else fadd2(acc0, p0, p1);
                         pk[c] = pack2<T>(p0, p1);
                     }
