@@ -13,8 +13,8 @@
 //               maximum m and sum l in fp32, the accumulator rescaled only when
 //               m grows by more than 2^8; P in the operands' type into the
 //               first 64 columns of S_t, in two halves of 64 keys; then O / l.
-//               Warps w and w + 4 share an SM sub-partition and take turns on
-//               its exponential unit.
+//               (Taking turns on the exponential unit, as the dense kernel's
+//               tiles do over thousands of keys, cost 3 to 4 % here.)
 //   warp 8      tcgen05.mma issuer: S_t = Q_t K^T, O_t += P_t V.
 //   warp 9      where a value tile holds rows that must not count (behind the
 //               segment's end, or masked) it writes zeros over them: P is 0
@@ -105,9 +105,8 @@ struct CrossCfg {
 
 enum : int {
     CB_QFULL = 0, CB_QEMPTY = 2, CB_KFULL = 4, CB_KEMPTY = 8, CB_VFULL = 12, CB_VEMPTY = 16,
-    CB_VFIX = 20, CB_TURN = 24,   // CB_TURN * 8 is a multiple of 64
-    CB_SFULL = 32, CB_P1 = 34, CB_P2 = 36, CB_OFULL = 38, CB_DRAIN = 40, CB_IFULL = 41,
-    CB_IEMPTY = 45, CB_COUNT = 49
+    CB_VFIX = 20, CB_SFULL = 24, CB_P1 = 26, CB_P2 = 28, CB_OFULL = 30, CB_DRAIN = 32,
+    CB_IFULL = 33, CB_IEMPTY = 37, CB_COUNT = 41
 };
 
 // The plan of a launch in shared memory, from one address on: the key tiles of a
@@ -281,7 +280,6 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&bars[CB_IFULL + i], 1);
             mbar_init(&bars[CB_IEMPTY + i], 11);   // every warp but the one that fills it
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&bars[CB_TURN + i], 1);
         *abort = 0;
         fence_mbar_init();
     }
@@ -621,25 +619,10 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t tS = tmem + lane_off + C::COL_S + t * 128;
         const uint32_t tO = tS + (C::COL_O - C::COL_S);
         const float sl2 = p.scale_log2;
-        uint32_t par = 0;   // parities of the next phases: 1 S, 2 O, 4 turn
-        // Barrier addresses from few registers: those of tile t, and this sub-partition's
-        // turns. Tile 0 waits for tile 1's last key tile in turn, tile 1 for tile 0's same
-        // one; each gives on the other's barrier, 32 bytes (of 64) away.
-        const uint32_t bar_t = bar0 + t * 8;
-        const uint32_t turn = bar0 + (CB_TURN + 4 * t + (warp & 3)) * 8;
+        uint32_t par = 0;   // parities of the next phases: 1 S, 2 O
+        const uint32_t bar_t = bar0 + t * 8;   // of this tile's barriers, less their number * 8
         auto wait_t = [&](int bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait_at(bar_t + bar * 8, parity, abort_at));
-        };
-        // (tile 0's first wait is for the phase before the first, which counts as over)
-        auto take_turn = [&]() {
-            const bool r = __all_sync(0xffffffffu,
-                                      mbar_wait_at(turn, ((par >> 2) & 1) ^ (t == 0), abort_at));
-            par ^= 4u;
-            return r;
-        };
-        auto give_turn = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive_at(turn ^ 32u);
         };
         bool ok = true;   // false from the first wait that gave up
         for (uint32_t n = 0; ; item_done(n), ++n) {
@@ -666,10 +649,6 @@ __global__ void __launch_bounds__(384, 1)
             for (int j = 0; ok && !active && j < n_kv; ++j) {
                 ok = wait_t(CB_SFULL, par & 1);
                 par ^= 1u;
-                if (ok && two) {
-                    ok = take_turn();
-                    give_turn();
-                }
                 if (lane == 0) {
                     mbar_arrive_at(bar_t + CB_P1 * 8);
                     mbar_arrive_at(bar_t + CB_P2 * 8);
@@ -706,10 +685,6 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_st32(tS + 32, z);
                         tmem_wait_st();
                         tc_fence_before();
-                        if (two) {
-                            ok = take_turn();
-                            give_turn();
-                        }
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive_at(bar_t + CB_P1 * 8);
@@ -744,7 +719,7 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t s2 = f2_splat(sl2), n2 = f2_splat(nm);
                 // P of keys [32 h, 32 h + 32). All exponentials on MUFU: with three pairs of
                 // eight as polynomials on the FMA pipe, as the dense kernel has them, the
-                // packed clips took 2 % longer (items too short for a steady alternation)
+                // packed clips took 2 % longer
                 auto exp_part = [&](const int h) {
                     uint32_t pk[16];
 #pragma unroll
@@ -759,10 +734,6 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     tmem_st16(tS + 16 * h, pk);
                 };
-                if (two) {
-                    ok = take_turn();
-                    if (!ok) return;
-                }
                 exp_part(0);
                 exp_part(1);
                 if (__any_sync(0xffffffffu, need)) {
@@ -783,7 +754,6 @@ __global__ void __launch_bounds__(384, 1)
                 if (lane == 0) mbar_arrive_at(bar_t + CB_P1 * 8);
                 exp_part(2);
                 exp_part(3);
-                if (two) give_turn();
                 l += f2_sum(acc0) + f2_sum(acc1);
                 tmem_wait_st();
                 tc_fence_before();
