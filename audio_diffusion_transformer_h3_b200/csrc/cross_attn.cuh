@@ -29,12 +29,11 @@
 // chunks so that all SMs read. Each tile then leaves its unnormalised O, m and
 // l in fp32, and cross_join_kernel adds a row's parts up in their order.
 //
-// Measured: 8320 rows x 56 heads of 128 on 2048 keys 440 us (1107 TFLOP/s, the
-// dense self attention's rate at such lengths), on 512 keys 133 us: a key tile
-// costs 2.0 us for both query tiles, bound by the softmax, an item another 2.5 us,
-// in which the tensor cores wait for the last P, the output and the next first
-// scores (41 % busy at 512 keys). 64 rows on 33280 keys of 24 heads of 64: 63 us
-// (3.2 TB/s), with a mask 87.
+// Measured: 8320 rows x 56 heads of 128 on 2048 keys 421 us (1160 TFLOP/s, the
+// dense self attention's rate), on 512 keys 125 us: a key tile costs 1.9 us for
+// both query tiles, bound by the softmax, an item another 2 us, in which the
+// tensor cores wait for the last P, the output and the next first scores. 64 rows
+// on 33280 keys of 24 heads of 64: 63 us (3.2 TB/s), with a mask 74.
 //
 // Every wait is bounded; one that gives up sets H3_ERR_DEVICE_TIMEOUT, stops
 // the CTA, and leaves TMEM and shared memory only after the copies and MMAs in
@@ -98,9 +97,10 @@ struct CrossCfg {
     static constexpr int SMEM_BYTES = OFF_OUT + 8 * 4096 + 1024;   // + alignment slack
     static constexpr uint32_t COL_S = 0, COL_O = 256;   // S_t at 128 t, O_t at 256 + 128 t
     static constexpr int THREADS = 384;
-    // 168 registers a thread at launch; the producer warpgroup drops to 40 and
-    // the two softmax warpgroups rise to 232: 2 * 128 * 232 + 128 * 40 = 384 * 168
-    static constexpr int REGS_SOFTMAX = 232, REGS_PRODUCER = 40;
+    // 168 registers a thread at launch; the producer warpgroup drops to 56 and
+    // the two softmax warpgroups rise to 224: 2 * 128 * 224 + 128 * 56 = 384 * 168
+    // (with 232 and 40 masked keys took 11 % longer, the rest the same)
+    static constexpr int REGS_SOFTMAX = 224, REGS_PRODUCER = 56;
 };
 
 enum : int {
