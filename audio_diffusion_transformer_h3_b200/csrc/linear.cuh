@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(192, 1)
 // ------------------------------------------------------------- skinny kernel
 
 struct LinearSkinny {
-    static constexpr int BM = 128, BK = 64, MAX_COLS = 128;
+    static constexpr int BM = 128, BK = 64;
     static constexpr int W_BYTES = BM * BK * 2;
     static constexpr int MAX_STAGES = 6;
     static constexpr int RING_BYTES = 108 * 1024;                 // two CTAs an SM
