@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&bars[CB_KFULL + s], 1);
             mbar_init(&bars[CB_KEMPTY + s], 2);   // one commit for each tile
             mbar_init(&bars[CB_VFULL + s], 1);
-            mbar_init(&bars[CB_VEMPTY + s], 2);
+            mbar_init(&bars[CB_VEMPTY + s], 3);   // and warp 9, which passes every value tile
             mbar_init(&bars[CB_VFIX + s], 1);
         }
         mbar_init(&bars[CB_DRAIN], 1);
@@ -452,11 +452,16 @@ __global__ void __launch_bounds__(384, 1)
                 const bool fix = p.mask != nullptr || keys % 16 != 0;
                 const uint32_t now = bytes;
                 if (j + 1 < n_kv) bytes = mask_of(j + 1);
-                // every phase is waited for, those of tiles that need nothing too: a
-                // parity tells a phase from its neighbours only
+                // every phase is waited for, those of tiles that need nothing too, and
+                // the stage is filled again only after that: a parity tells a phase
+                // from its neighbours only, so a turn of the ring behind, this warp
+                // would take a later tile for its own
                 ok = wait(CB_VFULL + s, phase_of(nv));
                 if (!ok) break;
-                if (!fix) continue;
+                if (!fix) {
+                    if (lane == 0) mbar_arrive_at(bar0 + (CB_VEMPTY + s) * 8);
+                    continue;
+                }
                 uint8_t *v = smem + C::OFF_V + s * C::TILE_BYTES + (lane & 7) * 16;
                 // four rows a step, eight lanes a row
 #pragma unroll
@@ -471,7 +476,10 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_at(bar0 + (CB_VFIX + s) * 8);
+                if (lane == 0) {
+                    mbar_arrive_at(bar0 + (CB_VFIX + s) * 8);
+                    mbar_arrive_at(bar0 + (CB_VEMPTY + s) * 8);
+                }
             }
         }
         if (!ok && lane == 0) give_up(abort, p.status);
