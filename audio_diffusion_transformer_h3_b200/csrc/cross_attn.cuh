@@ -714,15 +714,17 @@ __global__ void __launch_bounds__(384, 1)
                 const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
                                        fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
                 const float m_new = mx * sl2;
-                // the accumulator holds something from the item's second key tile on
-                const bool grow = m_new > m + 8.0f || m == -INFINITY;
+                // (false while no score is above -infinity: m stays there.) The
+                // accumulator holds something from the item's second key tile on
+                const bool grow = m_new > m + 8.0f;
                 const bool need = grow && j > 0;
                 const float f = need ? ex2_approx(m - m_new) : 1.0f;
                 if (grow) {
                     l *= need ? f : 0.0f;
                     m = m_new;
                 }
-                const float nm = P_SHIFT - m;
+                // scores of -infinity weigh 0 also before any other score
+                const float nm = P_SHIFT - (m == -INFINITY ? 0.0f : m);
                 uint64_t acc0 = 0, acc1 = 0;
                 const uint64_t s2 = f2_splat(sl2), n2 = f2_splat(nm);
                 // P of keys [32 h, 32 h + 32). All exponentials on MUFU: with three pairs of
@@ -856,9 +858,11 @@ __global__ void __launch_bounds__(384, 1)
                         static_cast<int>(first * p.slot_rows) + r, mode == CM_KEYS ? -parts : parts);
             }
 #pragma unroll 1
-            for (int c = 0; n_kv > 0 && c < D; c += 16) {
+            for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
-                tmem_ld16(tO + c, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0u;   // without a key tile
+                if (n_kv > 0) tmem_ld16(tO + c, o);
                 tmem_wait_ld();
                 if (row_ok) {
 #pragma unroll
@@ -904,23 +908,22 @@ __global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p) {
     if (lane == 0) m_s[warp] = m;
     __syncthreads();
     m = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+    const float m0 = m == -INFINITY ? 0.0f : m;   // then every part weighs 0
     float sum = 0.0f, o[D / 32];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
     for (int i0 = warp; i0 < parts; i0 += 128) {
-        // a part without keys may hold no O: its weight 0 also says not to read it
         float w = 0.0f;
         const int mine = i0 + lane * 4;
         if (mine < parts) {
             const float2 ml = *reinterpret_cast<const float2 *>(part(mine));
-            w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+            w = ex2_approx(ml.x - m0);
             sum = fmaf(w, ml.y, sum);
         }
         const int n = min((parts - i0 + 3) / 4, 32);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
             const float wi = __shfl_sync(0xffffffffu, w, i);
-            if (wi == 0.0f) continue;
             const float *a = part(i0 + 4 * i) + 2 + lane * 2;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {

@@ -405,7 +405,7 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
  *     O = softmax(softmax_scale * q k^T) v over the segment's keys that the
  *     mask keeps, LSE = natural log of the row's sum of exponentials.
  * A row without keys (an empty key segment, or none kept) gets O = 0 and
- * LSE = -infinity.
+ * LSE = -infinity, and so does a row whose every score is -infinity.
  *   q, o     : device [Nq, Hq, D], token strides ldq, ldo >= Hq * D;
  *   k, v     : device [Nk, Hk, D], token strides ldk, ldv >= Hk * D; all
  *              16-byte aligned with strides a multiple of 8, heads contiguous;

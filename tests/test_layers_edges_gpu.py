@@ -4,9 +4,10 @@ bounds that test_layers_gpu.py derives."""
 
 import math
 
+import numpy as np
 import pytest
 
-from test_layers_gpu import _check_cross, _cross_case, _run_cross
+from test_layers_gpu import _check_cross, _cross_case, _f64, _run_cross, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,52 @@ def test_cross_long_unmasked_segments_that_end_inside_a_tile(lq, lk, Hq, Hk, D, 
             first = o
             _check_cross(q, k[:n], v[:n], cu_q, cu_k, o, lse, D ** -0.5, None, "o")
         assert torch.equal(o, first)
+
+
+def _low_scores(q, k, at, channel=3):
+    """Keys `at` score -infinity with every query: q is positive in a channel where
+    they are -infinity."""
+    q[:, :, channel] = q[:, :, channel].abs().clamp_min(0.25)
+    k[at, :, channel] = -math.inf
+
+
+# the kept keys that score -infinity, and whether the others are masked
+@pytest.mark.parametrize("case", ["first tile", "only kept key of the first tile", "a tile between",
+                                  "all but the last key", "single keys"])
+@pytest.mark.parametrize("lq,lk", [([300], [700]), ([1], [9000]), ([40, 3], [2000, 700])])
+@pytest.mark.parametrize("Hq,Hk,D,dtype", [(4, 4, 128, "bf16"), (16, 2, 64, "fp16")])
+def test_cross_keys_that_score_minus_infinity(case, lq, lk, Hq, Hk, D, dtype):
+    """Such keys weigh nothing, wherever they lie and whether or not the keys are
+    split over blocks: the result is that of the other keys alone."""
+    import torch
+    q, k, v, cu_q, cu_k = _cross_case(lq, lk, Hq, Hk, D, dtype)
+    n = sum(lk)
+    low, mask = torch.zeros(n, dtype=torch.bool), torch.ones(n, dtype=torch.bool)
+    for a, b in zip(np.cumsum([0] + lk), np.cumsum(lk)):
+        a, b = int(a), int(b)
+        if case == "first tile":
+            low[a:a + 128] = True
+        elif case == "only kept key of the first tile":
+            mask[a:a + 128] = False
+            mask[a + 5] = low[a + 5] = True
+        elif case == "a tile between":
+            low[a + 256:a + 384] = True
+        elif case == "all but the last key":
+            low[a:b - 1] = True
+        else:
+            low[a], low[a + 130], low[b - 1] = True, True, True
+    _low_scores(q, k, low.cuda())
+    for m in ([mask] if not mask.all() else [None, mask]):
+        o, lse = _run_cross(q, k, v, cu_q, cu_k, lq, lk, key_mask=None if m is None else m.cuda())
+        kept = (~low if m is None else m & ~low).cuda()
+        _check_cross(q, torch.where(low.cuda()[:, None, None], 0, k), v, cu_q, cu_k, o, lse, D ** -0.5,
+                     kept, case)
+
+
+@pytest.mark.parametrize("lq,lk", [([300], [700]), ([1], [9000]), ([2], [1])])
+def test_cross_rows_whose_every_key_scores_minus_infinity(lq, lk):
+    """No key has weight: 0 and -infinity, as where there is no key."""
+    q, k, v, cu_q, cu_k = _cross_case(lq, lk, 4, 2, 128, "bf16")
+    _low_scores(q, k, slice(None))
+    o, lse = _run_cross(q, k, v, cu_q, cu_k, lq, lk)
+    assert (o == 0).all() and (lse == -math.inf).all()
