@@ -793,8 +793,9 @@ __global__ void __launch_bounds__(384, 1)
             const int parts = lds32(xs + CX_SPLITS) * (mode == CM_KEYS ? 2 : 1);
             if (!ok || !active) continue;
             if (parts == 1) {
-                // a row without keys: O is 0 or, without a single key tile, not there
-                const uint64_t inv2 = f2_splat(l > 0.0f ? 1.0f / l : 0.0f);
+                // a row without keys: O is 0 or, without a single key tile, not there (a
+                // sum of NaN is neither: it shows in O and in the LSE)
+                const uint64_t inv2 = f2_splat(l == 0.0f ? 0.0f : 1.0f / l);
                 // 64 channels at a time through shared memory (16-byte pieces, their
                 // place exclusive-or'ed with the row), so that a store writes four
                 // whole 128-byte lines; 16 bytes of each of 32 rows at a time took 4 to
@@ -842,7 +843,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (row_ok && p.lse != nullptr)
                     p.lse[static_cast<int64_t>(head) * p.Nq + qrow] =
-                        l > 0.0f ? (m + (log2f(l) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
+                        l == 0.0f ? -INFINITY : (m + (log2f(l) - P_SHIFT)) * 0.69314718055994530942f;
                 if (p.split && row_ok)   // not among the parts
                     p.rows[static_cast<int64_t>(qrow) * p.Hq + head] = make_int2(0, 0);
                 continue;
@@ -942,14 +943,14 @@ __global__ void __launch_bounds__(128) cross_join_kernel(const CrossParams p) {
     }
     __syncthreads();
     sum = ((sum_s[0] + sum_s[1]) + sum_s[2]) + sum_s[3];
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int token = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(token) * p.Hq);
     T *to = static_cast<T *>(p.o) + token * p.ldo + static_cast<int64_t>(head) * D;
     const int c = threadIdx.x;
     if (c < D) to[c] = from_f32<T>((((o_s[0][c] + o_s[1][c]) + o_s[2][c]) + o_s[3][c]) * inv);
     if (c == 0 && p.lse != nullptr)
         p.lse[static_cast<int64_t>(head) * p.Nq + token] =
-            sum > 0.0f ? (m + (log2f(sum) - P_SHIFT)) * 0.69314718055994530942f : -INFINITY;
+            sum == 0.0f ? -INFINITY : (m + (log2f(sum) - P_SHIFT)) * 0.69314718055994530942f;
 }
 
 }  // namespace h3

@@ -406,6 +406,7 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
  *     mask keeps, LSE = natural log of the row's sum of exponentials.
  * A row without keys (an empty key segment, or none kept) gets O = 0 and
  * LSE = -infinity, and so does a row whose every score is -infinity.
+ * A NaN score, or scores of +infinity, make O and LSE of their row NaN.
  *   q, o     : device [Nq, Hq, D], token strides ldq, ldo >= Hq * D;
  *   k, v     : device [Nk, Hk, D], token strides ldk, ldv >= Hk * D; all
  *              16-byte aligned with strides a multiple of 8, heads contiguous;

@@ -7,7 +7,7 @@ import math
 import numpy as np
 import pytest
 
-from test_layers_gpu import _check_cross, _cross_case, _f64, _run_cross, _within
+from test_layers_gpu import _check_cross, _cross_case, _run_cross
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,35 @@ def test_cross_rows_whose_every_key_scores_minus_infinity(lq, lk):
     _low_scores(q, k, slice(None))
     o, lse = _run_cross(q, k, v, cu_q, cu_k, lq, lk)
     assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("lq,lk", [([300], [700]), ([3], [9000]), ([1, 70], [900, 100])])
+@pytest.mark.parametrize("Hq,Hk,D,dtype", [(4, 4, 128, "bf16"), (16, 2, 64, "fp16")])
+def test_cross_nan_shows_in_the_result_and_in_the_lse(lq, lk, Hq, Hk, D, dtype):
+    """A NaN in a query or in a key that counts makes its rows NaN, the LSE too: it
+    does not read as a row without keys. Other rows are as they were."""
+    import torch
+    q, k, v, cu_q, cu_k = _cross_case(lq, lk, Hq, Hk, D, dtype)
+    clean, lse0 = _run_cross(q, k, v, cu_q, cu_k, lq, lk)
+    bad = q.clone()
+    bad[0, 1, 7] = math.nan
+    o, lse = _run_cross(bad, k, v, cu_q, cu_k, lq, lk)
+    there = torch.zeros(Hq, sum(lq), dtype=torch.bool, device="cuda")
+    there[1, 0] = True
+    assert torch.isnan(lse[there]).all() and torch.isnan(o[there.t()]).all()
+    assert torch.equal(lse[~there], lse0[~there]) and torch.equal(o[~there.t()], clean[~there.t()])
+    bad = k.clone()
+    bad[lk[0] - 1, Hk - 1, 0] = math.nan      # the first segment's last key, the last group's heads
+    o, lse = _run_cross(q, bad, v, cu_q, cu_k, lq, lk)
+    there[:] = False
+    there[-(Hq // Hk):, :lq[0]] = True
+    assert torch.isnan(lse[there]).all() and torch.isnan(o[there.t()]).all()
+    assert torch.equal(lse[~there], lse0[~there]) and torch.equal(o[~there.t()], clean[~there.t()])
+    # every key that counts is NaN
+    mask = torch.zeros(sum(lk), dtype=torch.bool, device="cuda")
+    mask[:lk[0]:3] = True
+    bad = k.clone()
+    bad[:lk[0]] = math.nan
+    o, lse = _run_cross(q, bad, v, cu_q, cu_k, lq, lk, key_mask=mask)
+    assert torch.isnan(lse[:, :lq[0]]).all() and torch.isnan(o[:lq[0]]).all()
+    assert (lse[:, lq[0]:] == -math.inf).all() and (o[lq[0]:] == 0).all()
