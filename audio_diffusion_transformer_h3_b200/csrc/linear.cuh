@@ -40,7 +40,31 @@ struct LinearParams {
     int32_t cols, splits;     // splits: the cluster's CTAs
 };
 
-// act in place on V values; the switch is uniform over the grid.
+// (1 + erf(x / sqrt 2)) / 2, relatively accurate also where it is small (1 + erff cancels
+// there: 10 % at x = -5). Method: with z = |x| / sqrt 2 and t = 1 / (1 + 0.4 z),
+// erfc(z) exp(z^2) / t is a polynomial in t on (0, 1]: degree 8, fitted for the least
+// relative error (iteratively reweighted least squares: 1.3e-7, 4.4e-7 in fp32), its
+// coefficients halved; exp(-z^2) adds 2^-23 (z^2 + 2). Measured: 8320 x 14336 x 512,
+// where the epilogue counts most, 375 us (1 + erff 390, erfcf 685).
+__device__ __forceinline__ float normal_cdf(float x) {
+    const float t = __fdividef(1.0f, fmaf(fabsf(x), 0.28284271247461901f, 1.0f));
+    float p = 0.0251363218f;
+    p = fmaf(p, t, -0.0914719701f);
+    p = fmaf(p, t, 0.0845777988f);
+    p = fmaf(p, t, -0.00283428328f);
+    p = fmaf(p, t, 0.0707306936f);
+    p = fmaf(p, t, 0.0842668638f);
+    p = fmaf(p, t, 0.103921942f);
+    p = fmaf(p, t, 0.112834759f);
+    p = fmaf(p, t, 0.112837933f);
+    const float h = p * t * ex2_approx(x * x * -0.72134752044448170f);   // exp(-z^2)
+    return x < 0.0f ? h : 1.0f - h;
+}
+
+// act in place on V values; the switch is uniform over the grid. Each keeps its relative
+// accuracy where it is small. __expf is off by up to 2 + 1.2 |t| units of 2^-23 and
+// __fdividef by 2, far below the result's rounding (2^-9, 2^-12) until the quotient
+// itself is below x 2^-126.
 template <int V>
 __device__ __forceinline__ void activate(float (&x)[V], int act) {
     switch (act) {
@@ -51,7 +75,7 @@ __device__ __forceinline__ void activate(float (&x)[V], int act) {
         case 2:
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                x[i] = 0.5f * x[i] * (1.0f + erff(x[i] * 0.70710678118654752f));
+                x[i] *= normal_cdf(x[i]);
             break;
         case 3:
             // x/2 (1 + tanh u) = x / (1 + exp(-2u))

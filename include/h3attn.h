@@ -353,7 +353,7 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
 typedef enum h3_act {
     H3_ACT_NONE = 0,
     H3_ACT_RELU = 1,
-    H3_ACT_GELU = 2,      /* x/2 (1 + erf(x / sqrt 2)) */
+    H3_ACT_GELU = 2,      /* x/2 (1 + erf(x / sqrt 2)) = x/2 erfc(-x / sqrt 2) */
     H3_ACT_GELU_TANH = 3, /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
     H3_ACT_SILU = 4,      /* x / (1 + exp(-x)) */
     H3_ACT_GATED = 256

@@ -7,7 +7,7 @@ import math
 import numpy as np
 import pytest
 
-from test_layers_gpu import _check_cross, _cross_case, _run_cross
+from test_layers_gpu import _check_cross, _cross_case, _dtype, _f64, _h3, _run_cross, _u, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,36 @@ def test_cross_nan_shows_in_the_result_and_in_the_lse(lq, lk, Hq, Hk, D, dtype):
     o, lse = _run_cross(q, bad, v, cu_q, cu_k, lq, lk, key_mask=mask)
     assert torch.isnan(lse[:, :lq[0]]).all() and torch.isnan(o[:lq[0]]).all()
     assert (lse[:, lq[0]:] == -math.inf).all() and (o[lq[0]:] == 0).all()
+
+
+# --------------------------------------------------------------------- linear
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,dtype", [(4, "bf16"), (4, "fp16"), (200, "bf16"), (200, "fp16")])
+def test_linear_activations_keep_their_tails(act, M, dtype):
+    """Relative accuracy where an activation is small. Pre-activations are exact (one
+    product with 1 each), -9 to 9, so that 1 + exp(-2u) stays below 2^126.
+    Bound, relative, in units of 2^-23, t the exponent's argument: 1.2 |t| + 2 for
+    exp, 2 |t| for t's three roundings, 8 for what is left. GELU by erfc: 4 for erfc,
+    and 2 (x^2 / 2 + 1) for its argument's two roundings (|z erfc'(z) / erfc(z)| is
+    at most 2 z^2 + 1)."""
+    import torch
+    h3 = _h3()
+    d = _dtype(dtype)
+    x = torch.zeros(M, 8, dtype=d, device="cuda")
+    x[:, 0] = torch.linspace(-9, 9, M).to(d)
+    w = torch.zeros(136, 8, dtype=d, device="cuda")
+    w[:, 0] = torch.tensor([1.0, 0.5, 0.75, -1.0], dtype=d).repeat(34)
+    z = (x[:, :1].double() * w[:, 0].double()).cpu()
+    got = _f64(h3.linear_t(x, w, act=act))
+    zz = z.numpy()
+    if act == "gelu":
+        want = 0.5 * zz * np.vectorize(math.erfc)(-zz / math.sqrt(2))
+        rel = 12 + 2 * (zz ** 2 / 2 + 1)
+    else:
+        t = zz if act == "silu" else math.sqrt(8 / math.pi) * (zz + 0.044715 * zz ** 3)
+        want = zz / (1 + np.exp(-t))
+        rel = 10 + 3.2 * np.abs(t)
+    least = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -134
+    bound = (_u(d) + rel * 2.0 ** -23) * np.abs(want) + least
+    _within(got, want, bound, act)
