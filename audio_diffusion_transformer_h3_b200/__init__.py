@@ -605,8 +605,9 @@ def _on(device, stream):
     torch = _torch or _load_torch()
     if stream is None:
         return None if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+    if isinstance(stream, int):   # (ExternalStream takes 0 for "a new one")
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, not on {device}")
     return torch.cuda.stream(stream)

@@ -7,7 +7,7 @@ import math
 import numpy as np
 import pytest
 
-from test_layers_gpu import _check_cross, _cross_case, _dtype, _f64, _h3, _run_cross, _u, _within
+from test_layers_gpu import _check_cross, _cross_case, _cu, _dtype, _f64, _h3, _run_cross, _u, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,39 @@ def test_linear_activations_keep_their_tails(act, M, dtype):
     least = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -134
     bound = (_u(d) + rel * 2.0 ** -23) * np.abs(want) + least
     _within(got, want, bound, act)
+
+
+# ------------------------------------------------------- streams, autograd, memory
+
+def _calls(h3):
+    """Each helper as (name of the entry point, call with keywords)."""
+    import torch
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(16, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    a, b = x.view(4, 1, 64), w.view(16, 1, 64)
+    cu_q, cu_k = _cu([4]), _cu([16])
+    return [("h3_linear_fwd", lambda **kw: h3.linear_t(x, w, **kw)),
+            ("h3_rope_qk_apply", lambda **kw: h3.rope_qk_t(a, None, pos, **kw)),
+            ("h3_cross_attn_fwd", lambda **kw: h3.cross_attn_fwd_t(a, b, b, cu_q, cu_k, 4, 16, **kw))]
+
+
+def test_stream_handles_are_taken_as_they_are(monkeypatch):
+    """A raw handle names that stream, 0 the device's default stream."""
+    import torch
+    h3 = _h3()
+    side = torch.cuda.Stream()
+    seen = []
+    for name, call in _calls(h3):
+        entry = getattr(h3, name)
+        monkeypatch.setattr(h3, name, lambda *a, entry=entry: (seen.append(a[-1]), entry(*a))[1])
+        for stream, handle in ((0, 0), (None, 0), (side.cuda_stream, side.cuda_stream),
+                               (side, side.cuda_stream), (torch.cuda.default_stream(), 0)):
+            call(stream=stream)
+            assert seen[-1] == handle, (name, stream)
+        with torch.cuda.stream(side):
+            call(stream=0)
+            assert seen[-1] == 0, name
+            call()
+            assert seen[-1] == side.cuda_stream, name
+    torch.cuda.synchronize()
