@@ -598,10 +598,12 @@ def _same(device, *tensors):
             raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
 
 
-def _on(device, stream):
+def _on(device, stream, *tensors):
     """Context in which a call on ``stream`` (None: the device's current one)
     allocates and launches: that device is current, and what the call allocates
-    belongs to that stream. None if it is so already."""
+    belongs to that stream. None if it is so already. The memory of ``tensors``
+    is not given out again before a given stream has done what is on it by the
+    time they are dropped."""
     torch = _torch or _load_torch()
     if stream is None:
         return None if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
@@ -610,6 +612,9 @@ def _on(device, stream):
                   else torch.cuda.default_stream(device))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, not on {device}")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -685,8 +690,9 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
     gradients with negated positions."""
     torch = _torch or _load_torch()
     device = q.device
-    _same(device, q, k, positions)
-    ctx = _on(device, stream)
+    given = out or ()
+    _same(device, q, k, positions, *given)
+    ctx = _on(device, stream, q, k, positions, *given)
     if ctx is not None:
         with ctx:
             return rope_qk_t(q, k, positions, rot_dim, theta, layout, scaling, out)
@@ -706,7 +712,6 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
         ldqo, ldko = Hq * D, Hk * D
     else:
         qo, ko = out
-        _same(device, qo, ko)
         if qo.shape != q.shape or qo.dtype != q.dtype or (k is None) != (ko is None) or (
                 k is not None and (ko.shape != k.shape or ko.dtype != q.dtype)):
             raise ValueError("out must have the shapes and type of (q, k)")
@@ -735,7 +740,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
     torch = _torch or _load_torch()
     device = x.device
     _same(device, x, w, bias, residual, out, workspace)
-    ctx = _on(device, stream)
+    ctx = _on(device, stream, x, w, bias, residual, out, workspace)
     if ctx is not None:
         with ctx:
             return linear_t(x, w, bias, act, gated, residual, out, workspace)
@@ -796,7 +801,7 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
     torch = _torch or _load_torch()
     device = q.device
     _same(device, q, k, v, cu_q, cu_k, key_mask, out, workspace)
-    ctx = _on(device, stream)
+    ctx = _on(device, stream, q, k, v, cu_q, cu_k, key_mask, out, workspace)
     if ctx is not None:
         with ctx:
             return cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q, max_k, key_mask, softmax_scale,

@@ -182,3 +182,46 @@ def test_stream_handles_are_taken_as_they_are(monkeypatch):
             call()
             assert seen[-1] == side.cuda_stream, name
     torch.cuda.synchronize()
+
+
+def test_inputs_of_a_call_on_another_stream_are_kept_until_it_is_done():
+    """Inputs that are dropped after a call on another stream: their memory is not
+    given out again before that stream has come to the call. (Nothing is written into
+    what is given out.)"""
+    import torch
+    h3 = _h3()
+    side = torch.cuda.Stream()
+    rows, n = 2048, 2048
+
+    def inputs():
+        x = torch.ones(rows, n, dtype=torch.bfloat16, device="cuda")
+        w = torch.ones(n, n, dtype=torch.bfloat16, device="cuda")
+        pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+        return x, w, pos, _cu([rows])
+
+    def linear(x, w, pos, cu):
+        return h3.linear_t(x, w, residual=x, stream=side)
+
+    def rope(x, w, pos, cu):
+        return h3.rope_qk_t(x.view(rows, 32, 64), w.view(n, 32, 64), pos, stream=side)
+
+    def cross(x, w, pos, cu):
+        return h3.cross_attn_fwd_t(x.view(rows, 32, 64), w.view(n, 32, 64), w.view(n, 32, 64), cu, cu,
+                                   rows, rows, stream=side.cuda_stream)
+
+    for call in (linear, rope, cross):
+        call(*inputs())
+        torch.cuda.synchronize()
+        tensors = inputs()
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)   # about 0.2 s
+        kept = call(*tensors)
+        old = {t.data_ptr() for t in tensors}
+        del tensors
+        new = [torch.empty(rows, n, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        busy = not side.query()
+        assert busy and not old & {t.data_ptr() for t in new}, call.__name__
+        del new, kept
+        torch.cuda.synchronize()
