@@ -585,10 +585,12 @@ def _dtype_code(dtype, fp32: bool = False) -> int:
 
 
 def _same(device, *tensors):
-    """Every given tensor is on ``device``; none asks for a gradient (these
-    calls are forward only, so a gradient would be lost in silence)."""
+    """Every given tensor is on ``device``; none asks for a gradient or carries a
+    tangent (these calls are forward only, so either would be lost in silence)."""
     torch = _torch or _load_torch()
     grad = torch.is_grad_enabled()
+    fwd = torch.autograd.forward_ad
+    dual = fwd._current_level >= 0
     for t in tensors:
         if t is None:
             continue
@@ -596,6 +598,8 @@ def _same(device, *tensors):
             raise ValueError(f"all tensors must be on one CUDA device: {t.device}, {device}")
         if grad and t.requires_grad:
             raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
+        if dual and fwd.unpack_dual(t).tangent is not None:
+            raise ValueError("forward only: a tangent would be lost")
 
 
 def _on(device, stream, *tensors):

@@ -225,3 +225,23 @@ def test_inputs_of_a_call_on_another_stream_are_kept_until_it_is_done():
         assert busy and not old & {t.data_ptr() for t in new}, call.__name__
         del new, kept
         torch.cuda.synchronize()
+
+
+def test_tangents_are_refused():
+    """Forward only: a forward-mode tangent would be lost, so the call is refused."""
+    import torch
+    import torch.autograd.forward_ad as fwd
+    h3 = _h3()
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(16, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    with fwd.dual_level():
+        dx, dw = (fwd.make_dual(t, torch.ones_like(t)) for t in (x, w))
+        a, b, c = dx.view(4, 1, 64), dw.view(16, 1, 64), w.view(16, 1, 64)
+        for call in (lambda: h3.linear_t(dx, w), lambda: h3.linear_t(x, dw),
+                     lambda: h3.linear_t(x, w, bias=dw[:, 0].contiguous()),
+                     lambda: h3.rope_qk_t(a, None, pos), lambda: h3.rope_qk_t(c[:4], a, pos),
+                     lambda: h3.cross_attn_fwd_t(x.view(4, 1, 64), c, b, _cu([4]), _cu([16]), 4, 16)):
+            with pytest.raises(ValueError), torch.no_grad():
+                call()
+        h3.linear_t(x, w)   # neither has a tangent
