@@ -633,6 +633,13 @@ def _like(x):
     return _torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
+def _changed(*outs):
+    """Tells autograd that these tensors have been written into."""
+    for t in outs:
+        if t is not None:
+            _torch.autograd.graph.increment_version(t)
+
+
 def _heads(x, name):
     """(token stride) of a [N, H, D] tensor whose heads are contiguous."""
     if x.dim() != 3:
@@ -724,6 +731,7 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
                             0 if ko is None else ko.data_ptr(), ldko, positions.data_ptr(), cfg,
                             N, Hq, Hk, D, code, _current_stream(device)),
            "h3_rope_qk_apply")
+    _changed(*given)
     return qo, ko
 
 
@@ -768,6 +776,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
         if residual.shape != (M, N) or residual.dtype != x.dtype:
             raise ValueError(f"residual must be [{M}, {N}] of x's type")
         ldr = _rows(residual, "residual")
+    given = out
     if out is None:
         out = x.new_empty((M, N))
     elif out.shape != (M, N) or out.dtype != x.dtype:
@@ -780,6 +789,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
                          _rows(out, "out"), M, N, K, a, code, workspace.data_ptr(),
                          workspace.numel(), _current_stream(device)),
            "h3_linear_fwd")
+    _changed(given)
     return out
 
 
@@ -822,6 +832,7 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
     if key_mask is not None and (key_mask.shape != (Nk,) or not key_mask.is_contiguous() or
                                  key_mask.dtype not in (torch.bool, torch.uint8)):
         raise ValueError(f"key_mask must be contiguous bool or uint8 [{Nk}]")
+    given = out
     if out is None:
         out = _like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
@@ -838,4 +849,5 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                              scale, code, workspace.data_ptr(), workspace.numel(),
                              _current_stream(device)),
            "h3_cross_attn_fwd")
+    _changed(given)
     return (out, lse) if return_lse else out

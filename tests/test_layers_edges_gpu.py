@@ -245,3 +245,31 @@ def test_tangents_are_refused():
             with pytest.raises(ValueError), torch.no_grad():
                 call()
         h3.linear_t(x, w)   # neither has a tangent
+
+
+def test_writing_into_a_given_tensor_counts_as_a_change():
+    """Autograd keeps tensors for the backward pass and notices when one is written
+    over; so it does where a call writes into ``out``."""
+    import torch
+    h3 = _h3()
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(16, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    a, b = torch.ones(4, 1, 64, device="cuda"), torch.ones(4, 2, 64, device="cuda")
+    o = torch.ones(4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.ones(4, 16, dtype=torch.bfloat16, device="cuda")
+    c = w.view(16, 1, 64)
+    for call, outs in (
+            (lambda: h3.linear_t(x, w, out=y), [y]),
+            (lambda: h3.linear_t(x, w, residual=y, out=y), [y]),
+            (lambda: h3.rope_qk_t(a, b, pos, out=(a, b)), [a, b]),
+            (lambda: h3.rope_qk_t(a, None, pos, out=(a, None)), [a]),
+            (lambda: h3.cross_attn_fwd_t(x.view(4, 1, 64), c, c, _cu([4]), _cu([16]), 4, 16, out=o), [o])):
+        for out in outs:
+            leaf = torch.ones_like(out, requires_grad=True)
+            loss = (leaf * out).sum()   # keeps out
+            call()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+    with torch.inference_mode():   # such tensors have no count of changes
+        h3.linear_t(x, w, out=torch.empty(4, 16, dtype=torch.bfloat16, device="cuda"))
