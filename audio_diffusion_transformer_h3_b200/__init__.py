@@ -633,6 +633,12 @@ def _like(x):
     return _torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
+def _bytes(workspace) -> int:
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.nbytes
+
+
 def _changed(*outs):
     """Tells autograd that these tensors have been written into."""
     for t in outs:
@@ -787,7 +793,7 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
                          0 if bias is None else bias.data_ptr(),
                          0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
                          _rows(out, "out"), M, N, K, a, code, workspace.data_ptr(),
-                         workspace.numel(), _current_stream(device)),
+                         _bytes(workspace), _current_stream(device)),
            "h3_linear_fwd")
     _changed(given)
     return out
@@ -846,7 +852,7 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                              0 if lse is None else lse.data_ptr(), cu_q.data_ptr(),
                              cu_k.data_ptr(), nseg, int(max_q), int(max_k),
                              0 if key_mask is None else key_mask.data_ptr(), Nq, Nk, Hq, Hk, D,
-                             scale, code, workspace.data_ptr(), workspace.numel(),
+                             scale, code, workspace.data_ptr(), _bytes(workspace),
                              _current_stream(device)),
            "h3_cross_attn_fwd")
     _changed(given)

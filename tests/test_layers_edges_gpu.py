@@ -273,3 +273,22 @@ def test_writing_into_a_given_tensor_counts_as_a_change():
                 loss.backward()
     with torch.inference_mode():   # such tensors have no count of changes
         h3.linear_t(x, w, out=torch.empty(4, 16, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_a_workspace_is_as_large_as_its_memory():
+    """The count of bytes that goes with the pointer is that of memory behind it: a
+    view that says more elements than it has is refused, a wider type counts whole."""
+    import torch
+    h3 = _h3()
+    size = 1 << 12
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for name, call in _calls(h3):
+        if name == "h3_rope_qk_apply":   # has none
+            continue
+        want = call(workspace=ws)
+        assert torch.equal(call(workspace=torch.empty(64, dtype=torch.float32, device="cuda")), want)
+        for bad in (ws[:1].expand(size), ws[::2]):
+            with pytest.raises(ValueError):
+                call(workspace=bad)
+        with pytest.raises(h3.H3Error):   # 252 bytes
+            call(workspace=torch.empty(63, dtype=torch.float32, device="cuda"))
