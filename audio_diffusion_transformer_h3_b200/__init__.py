@@ -250,6 +250,14 @@ def h3_varlen_attn_fwd_static(q: int, k: int, v: int, o: int, lse: int, cu_seqle
                                               pos, rope, N, H, D, softmax_scale, stream))
 
 
+def _int32_sizes(*sizes: int) -> bool:
+    """Whether these fit the C calls' 32-bit arguments (ctypes would cut them off)."""
+    for size in sizes:
+        if size >> 31 not in (0, -1):
+            return False
+    return True
+
+
 def h3_rope_qk_freqs(cfg: h3_rope_qk_cfg):
     """Angle per position of each pair, NumPy float64 [rot_dim/2] (host only)."""
     import numpy as np
@@ -261,23 +269,29 @@ def h3_rope_qk_freqs(cfg: h3_rope_qk_cfg):
 def h3_rope_qk_apply(q: int, ldq: int, q_out: int, ldq_out: int, k: int, ldk: int, k_out: int,
                      ldk_out: int, positions: int, cfg: h3_rope_qk_cfg, N: int, Hq: int, Hk: int,
                      D: int, dtype: int, stream: int) -> int:
+    if not _int32_sizes(Hq, Hk, D, dtype):
+        return H3_ERR_INVALID_ARG
     return _lib.h3_rope_qk_apply(q, ldq, q_out, ldq_out, k, ldk, k_out, ldk_out, positions,
                                  ctypes.byref(cfg), N, Hq, Hk, D, dtype, stream)
 
 
 def h3_linear_workspace_size(M: int, N: int, K: int, act: int) -> int:
-    return _lib.h3_linear_workspace_size(M, N, K, act)
+    return _lib.h3_linear_workspace_size(M, N, K, act) if _int32_sizes(N, K, act) else 0
 
 
 def h3_linear_fwd(x: int, ldx: int, w: int, ldw: int, bias: int, residual: int, ldr: int, y: int,
                   ldy: int, M: int, N: int, K: int, act: int, dtype: int, workspace: int,
                   workspace_bytes: int, stream: int) -> int:
+    if not _int32_sizes(N, K, act, dtype):
+        return H3_ERR_INVALID_ARG
     return _lib.h3_linear_fwd(x, ldx, w, ldw, bias, residual, ldr, y, ldy, M, N, K, act, dtype,
                               workspace, workspace_bytes, stream)
 
 
 def h3_cross_workspace_size(Nq: int, Hq: int, Hk: int, D: int, nseg: int, max_q: int,
                             max_k: int) -> int:
+    if not _int32_sizes(Hq, Hk, D, nseg, max_q, max_k):
+        return 0
     return _lib.h3_cross_workspace_size(Nq, Hq, Hk, D, nseg, max_q, max_k)
 
 
@@ -286,6 +300,8 @@ def h3_cross_attn_fwd(q: int, ldq: int, k: int, ldk: int, v: int, ldv: int, o: i
                       key_mask: int, Nq: int, Nk: int, Hq: int, Hk: int, D: int,
                       softmax_scale: float, dtype: int, workspace: int, workspace_bytes: int,
                       stream: int) -> int:
+    if not _int32_sizes(nseg, max_q, max_k, Hq, Hk, D, dtype):
+        return H3_ERR_INVALID_ARG
     return _lib.h3_cross_attn_fwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, cu_q, cu_k, nseg, max_q,
                                   max_k, key_mask, Nq, Nk, Hq, Hk, D, softmax_scale, dtype,
                                   workspace, workspace_bytes, stream)
@@ -681,6 +697,8 @@ def rope_qk_cfg(rot_dim: int, theta: float = 10000.0, layout: str = "interleaved
     kind = s.pop("kind", "none")
     if kind not in ROPE_SCALINGS or layout not in ("interleaved", "half"):
         raise ValueError(f"unknown scaling {kind!r} or layout {layout!r}")
+    if not _int32_sizes(int(rot_dim)):
+        raise ValueError(f"rot_dim {rot_dim} is out of range")
     values = {"factor": 1.0, "original_len": 0.0, "beta_fast": 0.0, "beta_slow": 0.0,
               "attn_factor": 1.0}
     for key, value in s.items():

@@ -1,0 +1,31 @@
+"""Calls of the layers around the attention that are refused before any CUDA
+call: sizes and factors beyond their types, outputs that overlap."""
+
+import math
+
+import pytest
+
+import audio_diffusion_transformer_h3_b200 as h3
+from test_layers_abi import _cfg, _cross, _linear, _rope
+
+WRAP = 1 << 32   # what a 32-bit size loses
+
+
+def test_sizes_beyond_32_bits_do_not_come_round():
+    for call, sizes in ((_linear, dict(N=50, K=100, act=1, dtype=0)),
+                        (_rope, dict(Hq=8, Hk=2, D=128, dtype=0)),
+                        (_cross, dict(nseg=2, max_q=60, max_k=40, Hq=4, Hk=2, D=128, dtype=0))):
+        for name, value in sizes.items():
+            for far in (value + WRAP, value + (1 << 40), value - WRAP):
+                assert call(**{name: far}) == h3.H3_ERR_INVALID_ARG, (call.__name__, name, far)
+    for far in (WRAP, -WRAP):
+        assert h3.h3_linear_workspace_size(5, 5 + far, 5, 0) == 0
+        assert h3.h3_linear_workspace_size(5, 5, 5 + far, 0) == 0
+        assert h3.h3_linear_workspace_size(5, 5, 5, far) == 0
+        good = (10, 4, 2, 64, 1, 10, 10)
+        assert h3.h3_cross_workspace_size(*good) > 0
+        for i in range(1, 7):
+            assert h3.h3_cross_workspace_size(*good[:i], good[i] + far, *good[i + 1:]) == 0
+    for far in (WRAP, -WRAP):
+        with pytest.raises(ValueError):
+            h3.rope_qk_cfg(64 + far, 1e4)
