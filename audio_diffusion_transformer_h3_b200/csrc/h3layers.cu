@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -105,7 +106,8 @@ bool rope_freqs(const h3_rope_qk_cfg &c, double *f) {
     const int r = c.rot_dim;
     if (r < 2 || r > 2 * h3::kRopeQkMaxPairs || (r & 1) || c.reserved != 0) return false;
     if (c.layout != H3_ROPE_INTERLEAVED && c.layout != H3_ROPE_HALF) return false;
-    if (!positive(c.theta) || !std::isfinite(c.attn_factor)) return false;
+    // (the kernel multiplies by it in fp32)
+    if (!positive(c.theta) || !(std::fabs(c.attn_factor) <= FLT_MAX)) return false;
     if (c.scaling < H3_ROPE_SCALE_NONE || c.scaling > H3_ROPE_SCALE_YARN) return false;
     const double pi = 3.14159265358979323846;
     double theta = c.theta, lo = 0.0, hi = 0.0;

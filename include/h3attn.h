@@ -320,7 +320,7 @@ typedef struct h3_rope_qk_cfg {
     double theta;    /* > 0 (> 1 with YARN) */
     double factor;   /* > 0; read by every scaling but NONE */
     double original_len, beta_fast, beta_slow; /* TURNS, YARN: > 0, fast > slow */
-    double attn_factor; /* cos and sin are multiplied by it; finite (1: none) */
+    double attn_factor; /* cos and sin are multiplied by it; finite in fp32 (1: none) */
 } h3_rope_qk_cfg;
 
 /* The angle per position of each pair, freqs[rot_dim/2], in double. Host only.

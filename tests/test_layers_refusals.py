@@ -1,8 +1,6 @@
 """Calls of the layers around the attention that are refused before any CUDA
 call: sizes and factors beyond their types, outputs that overlap."""
 
-import math
-
 import pytest
 
 import audio_diffusion_transformer_h3_b200 as h3
@@ -29,3 +27,12 @@ def test_sizes_beyond_32_bits_do_not_come_round():
     for far in (WRAP, -WRAP):
         with pytest.raises(ValueError):
             h3.rope_qk_cfg(64 + far, 1e4)
+
+
+def test_rope_factors_beyond_fp32():
+    """cos and sin are multiplied in fp32: a factor that is infinite there turns zeros into NaN."""
+    for bad in (1e39, -1e39, 1.7e308):
+        assert _rope(_cfg(attn_factor=bad)) == h3.H3_ERR_INVALID_ARG
+        with pytest.raises(h3.H3Error):
+            h3.h3_rope_qk_freqs(_cfg(attn_factor=bad))
+    assert len(h3.h3_rope_qk_freqs(_cfg(attn_factor=3.4e38))) == 32
