@@ -420,6 +420,7 @@ h3_status h3_rope_qk_apply(const void *q, int64_t ldq, void *q_out, int64_t ldq_
         return H3_ERR_INVALID_ARG;
     if (q == q_out && ldq != ldq_out && q != nullptr) return H3_ERR_INVALID_ARG;
     if (Hk > 0 && k == k_out && ldk != ldk_out && k != nullptr) return H3_ERR_INVALID_ARG;
+    if (Hk > 0 && N > 0 && (q_out == k_out || q_out == k || k_out == q)) return H3_ERR_INVALID_ARG;
     const uintptr_t size = dtype == H3_FP32 ? 4 : 2;
     if (!aligned(q, size) || !aligned(q_out, size) || !aligned(positions, 4) ||
         (Hk > 0 && (!aligned(k, size) || !aligned(k_out, size))))

@@ -332,9 +332,10 @@ h3_status h3_rope_qk_freqs(const h3_rope_qk_cfg *cfg, double *freqs);
  * a (x0 cos - x1 sin), a (x0 sin + x1 cos) with angle position * f_j and
  * a = attn_factor; channels [rot_dim, D) are copied.
  *   q, q_out : device [N, Hq, D], token strides ldq, ldq_out >= Hq * D, heads
- *              contiguous; q_out may equal q (with equal strides); any other
- *              overlap is undefined. k, k_out, ldk, ldk_out likewise with Hk;
- *              k and k_out NULL and Hk = 0: q alone.
+ *              contiguous; q_out may equal q (with equal strides). k, k_out,
+ *              ldk, ldk_out likewise with Hk; k and k_out NULL and Hk = 0: q
+ *              alone. q may equal k; q_out = k, k_out = q and q_out = k_out are
+ *              refused, and any other overlap of an output is undefined.
  *   positions: device int32 [N], any value. Angles are exact to 2^-33 turns
  *              at every position (fixed-point phase), cos and sin fp32.
  *   0 <= N <= 2^30 (0 is a no-op), 1 <= Hq <= 65535, 0 <= Hk <= 65535,

@@ -36,3 +36,14 @@ def test_rope_factors_beyond_fp32():
         with pytest.raises(h3.H3Error):
             h3.h3_rope_qk_freqs(_cfg(attn_factor=bad))
     assert len(h3.h3_rope_qk_freqs(_cfg(attn_factor=3.4e38))) == 32
+
+
+def test_rope_outputs_that_are_other_operands():
+    """Blocks of q and k run in no order: an output that is the other's input or
+    output would be read and written at once."""
+    for bad in (dict(k_out=0x20000, ldk_out=1024), dict(q_out=0x30000), dict(k_out=0x10000),
+                dict(q_out=0x10000, k_out=0x10000), dict(q=0x10000, k=0x10000, q_out=0x10000),
+                dict(q=0x10000, k=0x10000, q_out=0x10000, k_out=0x10000)):
+        a = dict(Hq=2, Hk=2, ldq=1024, ldk=1024, ldq_out=1024, ldk_out=1024)
+        a.update(bad)
+        assert _rope(**a) == h3.H3_ERR_INVALID_ARG, bad
