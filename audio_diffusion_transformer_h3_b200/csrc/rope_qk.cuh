@@ -3,9 +3,11 @@
 // Pair j of the rotated channels turns by position * f_j. The angle per
 // position is held as a 64-bit fixed-point fraction of a full turn, so
 // position * phase modulo 2^64 is the angle modulo one turn without any range
-// reduction: exact for every int32 position up to the phase's own rounding
-// (2^-65 turns a position, 2^-34 turns at 2^31). An fp32 product would be off
-// by 2^-8 radians at position 2^17.
+// reduction, up to the phase's own rounding (2^-65 turns a position, 2^-34 turns at
+// 2^31; the frequency it is made of, a double, is off by some 2^-53 of itself:
+// |position| f_j 2^-52 radians). The top 32 bits of the fraction go to fp32: 2^-32
+// turns are left out and 2^-26 rounded off, 1e-7 radians at every position. An fp32
+// product would be off by 2^-8 radians at position 2^17.
 #pragma once
 
 #include <cstdint>

@@ -336,8 +336,11 @@ h3_status h3_rope_qk_freqs(const h3_rope_qk_cfg *cfg, double *freqs);
  *              ldk, ldk_out likewise with Hk; k and k_out NULL and Hk = 0: q
  *              alone. q may equal k; q_out = k, k_out = q and q_out = k_out are
  *              refused, and any other overlap of an output is undefined.
- *   positions: device int32 [N], any value. Angles are exact to 2^-33 turns
- *              at every position (fixed-point phase), cos and sin fp32.
+ *   positions: device int32 [N], any value. position * f_j is reduced to a
+ *              fraction of a turn in fixed point and rounded to fp32, so an angle
+ *              is off by 2^-26 turns (1e-7 radians) at every position, for the
+ *              f_j of h3_rope_qk_freqs; those are doubles, whose last places
+ *              make |position| f_j 2^-52 radians (5e-7 at 2^31). cos and sin fp32.
  *   0 <= N <= 2^30 (0 is a no-op), 1 <= Hq <= 65535, 0 <= Hk <= 65535,
  *   2 <= D <= 512, N * ld < 2^47, dtype H3_BF16, H3_FP16 or H3_FP32; pointers aligned to
  *   their element (16-byte aligned rows and halves take the vector path).

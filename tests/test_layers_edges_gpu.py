@@ -2,6 +2,7 @@
 at their ends, against float64 references (oracle/layers.py) within the error
 bounds that test_layers_gpu.py derives."""
 
+import fractions
 import math
 
 import numpy as np
@@ -146,6 +147,40 @@ def test_linear_activations_keep_their_tails(act, M, dtype):
     least = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -134
     bound = (_u(d) + rel * 2.0 ** -23) * np.abs(want) + least
     _within(got, want, bound, act)
+
+
+# --------------------------------------------------------------------- rotary
+
+# pi to 60 places
+PI = fractions.Fraction(3141592653589793238462643383279502884197169399375105820974944, 10 ** 60)
+
+
+@pytest.mark.parametrize("layout,scaling", [
+    ("half", None), ("interleaved", dict(kind="linear", factor=7.0)),
+    ("half", dict(kind="yarn", factor=4.0, original_len=32768, beta_fast=32.0, beta_slow=1.0))])
+def test_rope_angles_at_every_position(layout, scaling):
+    """cos and sin of position * f_j, for the f_j that h3_rope_qk_freqs gives, anywhere
+    in int32: off by 2^-26 + 2^-32 + 2^-34 turns (the fraction of a turn in fp32, its
+    bits that are left out, the phase's own rounding) and 2 units of fp32 for sincospi.
+    The reference reduces the angle in exact fractions."""
+    import torch
+    h3 = _h3()
+    rot, theta = 64, 1e6
+    rng = np.random.default_rng(21)
+    positions = np.unique(np.concatenate([
+        rng.integers(-2 ** 31, 2 ** 31, 150), rng.integers(0, 1 << 18, 150), 2 ** np.arange(31),
+        [0, -1, 2 ** 31 - 1, -2 ** 31]])).astype(np.int32)
+    freqs = [fractions.Fraction(float(f)) for f in
+             h3.h3_rope_qk_freqs(h3.rope_qk_cfg(rot, theta, layout, scaling))]
+    turns = np.array([[float((int(p) * f / (2 * PI)) % 1) for f in freqs] for p in positions])
+    x = torch.zeros(len(positions), 1, rot, device="cuda")
+    first, second = ((slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half"
+                     else (slice(0, rot, 2), slice(1, rot, 2)))
+    x[..., first] = 1.0
+    y, _ = h3.rope_qk_t(x, None, torch.from_numpy(positions).cuda(), rot, theta, layout, scaling)
+    bound = 2 * math.pi * (2.0 ** -26 + 2.0 ** -32 + 2.0 ** -34) + 2.0 ** -23 + 1e-15
+    _within(_f64(y)[:, 0, first], np.cos(2 * math.pi * turns), bound, "cos")
+    _within(_f64(y)[:, 0, second], np.sin(2 * math.pi * turns), bound, "sin")
 
 
 # ------------------------------------------------------- streams, autograd, memory
