@@ -8,7 +8,8 @@ import math
 import numpy as np
 import pytest
 
-from test_layers_gpu import _check_cross, _cross_case, _cu, _dtype, _f64, _h3, _run_cross, _u, _within
+from test_layers_gpu import (_check_cross, _check_linear, _cross_case, _cu, _dtype, _f64, _h3,
+                             _linear_case, _run_cross, _u, _within)
 
 pytestmark = pytest.mark.gpu
 
@@ -147,6 +148,51 @@ def test_linear_activations_keep_their_tails(act, M, dtype):
     least = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -134
     bound = (_u(d) + rel * 2.0 ** -23) * np.abs(want) + least
     _within(got, want, bound, act)
+
+
+@pytest.mark.parametrize("M,N,K,gated,act", [
+    # on 148 SMs, tile columns / parts of the last round's tiles:
+    (2690, 1999, 200, False, "gelu_tanh"),   # 256 / 4, 22 row tiles (a partial last group), 8 column tiles
+    (3000, 2000, 136, False, "none"),        # 256 / 2
+    (2600, 4001, 72, False, "silu"),         # 192 / 1, three tiles a CTA
+    (6000, 900, 72, False, "relu"),          # 160 / 1, 47 row tiles
+    (4100, 2333, 72, True, "silu"),          # 128 / 4, gate and up
+    (2690, 1999, 136, True, "gelu_tanh"),    # 128 / 2
+    (2600, 4001, 72, True, "none"),          # 96 / 1, six tiles a CTA
+])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_linear_many_tiles(M, N, K, gated, act, dtype):
+    """Every output of layers that take several tiles a CTA, of several column tiles and
+    more row tiles than sweep the columns together, the last ones in parts."""
+    h3 = _h3()
+    x, w, b, r = _linear_case(M, N, K, act, gated, True, True, dtype)
+    _check_linear(x, w, b, act, gated, r, h3.linear_t(x, w, b, act, gated, r), "y")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 14336), (2, 5376, 5376), (17, 260, 14336), (96, 200, 8200),
+                                   (128, 300, 14336), (300, 513, 14336), (130, 1100, 4104),
+                                   (2690, 1999, 1000)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_whole_numbers_are_exact(M, N, K, gated):
+    """Inputs of -1, 0 and 1: sums of at most 14337 and the products of the gate stay
+    whole numbers below 2^24 (a sum is about 80, a product beyond 2^24 takes sums of 50
+    times that), exact in fp32 in any order, so y is the definition's value rounded
+    once. A K step that is lost or taken twice shows."""
+    import torch
+    h3 = _h3()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M + N + K)
+
+    def draw(*shape):
+        return torch.randint(-1, 2, shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    W = 2 * N if gated else N
+    x, w, b, r = draw(M, K), draw(W, K), draw(W), draw(M, N)
+    z = x.double() @ w.double().t() + b.double()
+    want = (z[:, :N].clamp_min(0) * z[:, N:] if gated else z.clamp_min(0)) + r.double()
+    assert want.abs().max() < 2 ** 24
+    y = h3.linear_t(x, w, b, "relu", gated, r)
+    assert torch.equal(y, want.to(torch.bfloat16))
 
 
 # --------------------------------------------------------------------- rotary
