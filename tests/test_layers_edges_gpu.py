@@ -117,6 +117,16 @@ def test_cross_nan_shows_in_the_result_and_in_the_lse(lq, lk, Hq, Hk, D, dtype):
     assert (lse[:, lq[0]:] == -math.inf).all() and (o[lq[0]:] == 0).all()
 
 
+def test_cross_as_many_segments_as_are_allowed():
+    """65535 segments, many of them empty on one side or both."""
+    rng = np.random.default_rng(8)
+    lq, lk = (rng.integers(0, 3, 65535).tolist() for _ in range(2))
+    lq[40000], lk[40000], lk[40001] = 300, 500, 0
+    q, k, v, cu_q, cu_k = _cross_case(lq, lk, 1, 1, 64, "bf16")
+    o, lse = _run_cross(q, k, v, cu_q, cu_k, lq, lk)
+    _check_cross(q, k, v, cu_q, cu_k, o, lse, 0.125, None, "o")
+
+
 # --------------------------------------------------------------------- linear
 
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
