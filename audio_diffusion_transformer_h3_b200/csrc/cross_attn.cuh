@@ -824,22 +824,20 @@ __global__ void __launch_bounds__(384, 1)
                                    o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     __syncwarp();
-#pragma unroll 1
-                    for (int i0 = 0; i0 < 8; i0 += 8) {   // loads, then stores: their latencies overlap
-                        uint4 v[8];
-                        int64_t row_at[8];
+                    // loads, then stores: their latencies overlap
+                    uint4 v[8];
+                    int64_t row_at[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int rr = (i0 + i) * 4 + lane / 8;
-                            v[i] = lds128(out + rr * 128 + (((lane ^ rr) & 7) << 4));
-                            row_at[i] = __shfl_sync(0xffffffffu, at, rr);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (row_at[i] >= 0)
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + row_at[i] + c +
-                                                           (lane & 7) * 8) = v[i];
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + lane / 8;
+                        v[i] = lds128(out + rr * 128 + (((lane ^ rr) & 7) << 4));
+                        row_at[i] = __shfl_sync(0xffffffffu, at, rr);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (row_at[i] >= 0)
+                            *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + row_at[i] + c +
+                                                       (lane & 7) * 8) = v[i];
                 }
                 if (row_ok && p.lse != nullptr)
                     p.lse[static_cast<int64_t>(head) * p.Nq + qrow] =
