@@ -250,12 +250,10 @@ def h3_varlen_attn_fwd_static(q: int, k: int, v: int, o: int, lse: int, cu_seqle
                                               pos, rope, N, H, D, softmax_scale, stream))
 
 
-def _int32_sizes(*sizes: int) -> bool:
-    """Whether these fit the C calls' 32-bit arguments (ctypes would cut them off)."""
-    for size in sizes:
-        if size >> 31 not in (0, -1):
-            return False
-    return True
+# ctypes cuts integers off to 32 bits where the C calls take that many. The bits of
+# several sizes together, shifted by 31, are 0 where all fit, and -1 where one is
+# negative, which the calls refuse themselves.
+_FITS = (0, -1)
 
 
 def h3_rope_qk_freqs(cfg: h3_rope_qk_cfg):
@@ -269,20 +267,20 @@ def h3_rope_qk_freqs(cfg: h3_rope_qk_cfg):
 def h3_rope_qk_apply(q: int, ldq: int, q_out: int, ldq_out: int, k: int, ldk: int, k_out: int,
                      ldk_out: int, positions: int, cfg: h3_rope_qk_cfg, N: int, Hq: int, Hk: int,
                      D: int, dtype: int, stream: int) -> int:
-    if not _int32_sizes(Hq, Hk, D, dtype):
+    if (Hq | Hk | D | dtype) >> 31 not in _FITS:
         return H3_ERR_INVALID_ARG
     return _lib.h3_rope_qk_apply(q, ldq, q_out, ldq_out, k, ldk, k_out, ldk_out, positions,
                                  ctypes.byref(cfg), N, Hq, Hk, D, dtype, stream)
 
 
 def h3_linear_workspace_size(M: int, N: int, K: int, act: int) -> int:
-    return _lib.h3_linear_workspace_size(M, N, K, act) if _int32_sizes(N, K, act) else 0
+    return _lib.h3_linear_workspace_size(M, N, K, act) if (N | K | act) >> 31 in _FITS else 0
 
 
 def h3_linear_fwd(x: int, ldx: int, w: int, ldw: int, bias: int, residual: int, ldr: int, y: int,
                   ldy: int, M: int, N: int, K: int, act: int, dtype: int, workspace: int,
                   workspace_bytes: int, stream: int) -> int:
-    if not _int32_sizes(N, K, act, dtype):
+    if (N | K | act | dtype) >> 31 not in _FITS:
         return H3_ERR_INVALID_ARG
     return _lib.h3_linear_fwd(x, ldx, w, ldw, bias, residual, ldr, y, ldy, M, N, K, act, dtype,
                               workspace, workspace_bytes, stream)
@@ -290,7 +288,7 @@ def h3_linear_fwd(x: int, ldx: int, w: int, ldw: int, bias: int, residual: int, 
 
 def h3_cross_workspace_size(Nq: int, Hq: int, Hk: int, D: int, nseg: int, max_q: int,
                             max_k: int) -> int:
-    if not _int32_sizes(Hq, Hk, D, nseg, max_q, max_k):
+    if (Hq | Hk | D | nseg | max_q | max_k) >> 31 not in _FITS:
         return 0
     return _lib.h3_cross_workspace_size(Nq, Hq, Hk, D, nseg, max_q, max_k)
 
@@ -300,7 +298,7 @@ def h3_cross_attn_fwd(q: int, ldq: int, k: int, ldk: int, v: int, ldv: int, o: i
                       key_mask: int, Nq: int, Nk: int, Hq: int, Hk: int, D: int,
                       softmax_scale: float, dtype: int, workspace: int, workspace_bytes: int,
                       stream: int) -> int:
-    if not _int32_sizes(nseg, max_q, max_k, Hq, Hk, D, dtype):
+    if (nseg | max_q | max_k | Hq | Hk | D | dtype) >> 31 not in _FITS:
         return H3_ERR_INVALID_ARG
     return _lib.h3_cross_attn_fwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, cu_q, cu_k, nseg, max_q,
                                   max_k, key_mask, Nq, Nk, Hq, Hk, D, softmax_scale, dtype,
@@ -576,17 +574,16 @@ def device_status_t(workspace, stream=None) -> int:
 # -------------------------------------------- layers around the attention (torch)
 
 _DTYPE_CODES: dict = {}
-_torch = None
+_torch = _forward_ad = None
 
 
 def _load_torch():
     """torch, kept: an import statement in every helper costs these short calls
     a tenth of their time."""
-    global _torch
+    global _torch, _forward_ad
     import torch
-    _torch = torch
+    _torch, _forward_ad = torch, torch.autograd.forward_ad
     return torch
-
 
 
 def _dtype_code(dtype, fp32: bool = False) -> int:
@@ -605,16 +602,16 @@ def _same(device, *tensors):
     tangent (these calls are forward only, so either would be lost in silence)."""
     torch = _torch or _load_torch()
     grad = torch.is_grad_enabled()
-    fwd = torch.autograd.forward_ad
-    dual = fwd._current_level >= 0
+    dual = _forward_ad._current_level >= 0
+    cuda = device.type == "cuda"
     for t in tensors:
         if t is None:
             continue
-        if t.device != device or device.type != "cuda":
+        if t.device != device or not cuda:
             raise ValueError(f"all tensors must be on one CUDA device: {t.device}, {device}")
         if grad and t.requires_grad:
             raise ValueError("forward only: call under torch.no_grad() or detach the inputs")
-        if dual and fwd.unpack_dual(t).tangent is not None:
+        if dual and _forward_ad.unpack_dual(t).tangent is not None:
             raise ValueError("forward only: a tangent would be lost")
 
 
@@ -657,9 +654,7 @@ def _bytes(workspace) -> int:
 
 def _changed(*outs):
     """Tells autograd that these tensors have been written into."""
-    for t in outs:
-        if t is not None:
-            _torch.autograd.graph.increment_version(t)
+    _torch.autograd.graph.increment_version([t for t in outs if t is not None])
 
 
 def _heads(x, name):
@@ -697,7 +692,7 @@ def rope_qk_cfg(rot_dim: int, theta: float = 10000.0, layout: str = "interleaved
     kind = s.pop("kind", "none")
     if kind not in ROPE_SCALINGS or layout not in ("interleaved", "half"):
         raise ValueError(f"unknown scaling {kind!r} or layout {layout!r}")
-    if not _int32_sizes(int(rot_dim)):
+    if int(rot_dim) >> 31 not in _FITS:
         raise ValueError(f"rot_dim {rot_dim} is out of range")
     values = {"factor": 1.0, "original_len": 0.0, "beta_fast": 0.0, "beta_slow": 0.0,
               "attn_factor": 1.0}
@@ -755,7 +750,8 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
                             0 if ko is None else ko.data_ptr(), ldko, positions.data_ptr(), cfg,
                             N, Hq, Hk, D, code, _current_stream(device)),
            "h3_rope_qk_apply")
-    _changed(*given)
+    if given:
+        _changed(*given)
     return qo, ko
 
 
@@ -813,7 +809,8 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
                          _rows(out, "out"), M, N, K, a, code, workspace.data_ptr(),
                          _bytes(workspace), _current_stream(device)),
            "h3_linear_fwd")
-    _changed(given)
+    if given is not None:
+        _changed(given)
     return out
 
 
@@ -873,5 +870,6 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
                              scale, code, workspace.data_ptr(), _bytes(workspace),
                              _current_stream(device)),
            "h3_cross_attn_fwd")
-    _changed(given)
+    if given is not None:
+        _changed(given)
     return (out, lse) if return_lse else out
