@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 #include <mutex>
 
 #include "h3attn.h"
@@ -579,9 +580,10 @@ h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t l
     p.Hq = Hq; p.Hk = Hk;
     p.hp = c.hp; p.tokens = c.tokens; p.heads_blocks = Hq / c.hp;
     p.split = c.split;
-    // a scale of 0 (the mean of the values) as one that no score survives, so
-    // that a masked score of -infinity stays one
-    p.scale_log2 = std::max(softmax_scale * 1.4426950408889634f, 1e-30f);
+    // a scale of 0 (the mean of the values) as one that no score survives (fp32's
+    // largest times it is 5e-7), so that a masked score of -infinity stays one
+    p.scale_log2 = std::max(softmax_scale * 1.4426950408889634f,
+                            std::numeric_limits<float>::denorm_min());
     p.rows = reinterpret_cast<int2 *>(ws + kStatusBytes);
     p.parts = reinterpret_cast<float *>(ws + kStatusBytes + cross_rows_bytes(c));
     p.slot_rows = c.slot_rows;

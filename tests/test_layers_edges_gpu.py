@@ -127,6 +127,23 @@ def test_cross_as_many_segments_as_are_allowed():
     _check_cross(q, k, v, cu_q, cu_k, o, lse, 0.125, None, "o")
 
 
+@pytest.mark.parametrize("lq,lk", [([200], [500]), ([2], [3000])])
+@pytest.mark.parametrize("scale", [0.0, 1e-38, 1e-42])
+def test_cross_small_scales_of_large_scores(lq, lk, scale):
+    """Scores near fp32's largest times a scale near its smallest, and times 0 (the mean
+    of the values). 1e-42 is subnormal: 2^-11 of it is its last place."""
+    import torch
+    q, k, v, cu_q, cu_k = _cross_case(lq, lk, 2, 2, 64, "bf16")
+    q.mul_(2e18), k.mul_(2e18)
+    o, lse = _run_cross(q, k, v, cu_q, cu_k, lq, lk, softmax_scale=scale)
+    exact = scale if scale != 1e-42 else float(np.float32(1e-42))
+    if scale != 1e-42:
+        _check_cross(q, k, v, cu_q, cu_k, o, lse, exact, None, f"scale {scale}")
+    else:   # no score is above 2e-3: the mean, to that much
+        mean = v.double().mean(0).expand(o.shape)
+        assert torch.all((o.double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 5e-3 * v.double().abs().mean(0))
+
+
 # --------------------------------------------------------------------- linear
 
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
