@@ -618,12 +618,11 @@ def _same(device, *tensors):
 def _on(device, stream, *tensors):
     """Context in which a call on ``stream`` (None: the device's current one)
     allocates and launches: that device is current, and what the call allocates
-    belongs to that stream. None if it is so already. The memory of ``tensors``
-    is not given out again before a given stream has done what is on it by the
-    time they are dropped."""
+    belongs to that stream. The memory of ``tensors`` is not given out again
+    before a given stream has done what is on it by the time they are dropped."""
     torch = _torch or _load_torch()
     if stream is None:
-        return None if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+        return torch.cuda.device(device)
     if isinstance(stream, int):   # (ExternalStream takes 0 for "a new one")
         stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                   else torch.cuda.default_stream(device))
@@ -706,6 +705,16 @@ def rope_qk_cfg(rot_dim: int, theta: float = 10000.0, layout: str = "interleaved
                           values["attn_factor"])
 
 
+_PLAIN = frozenset((float, int, str))
+
+
+def _by_value(scaling):
+    """A scaling's items as plain numbers: what a cfg is kept under."""
+    if _PLAIN.issuperset(map(type, scaling.values())):
+        return tuple(scaling.items())
+    return tuple((k, v if isinstance(v, str) else float(v)) for k, v in scaling.items())
+
+
 @functools.lru_cache(maxsize=64)
 def _rope_qk_cfg(rot_dim, theta, layout, scaling) -> h3_rope_qk_cfg:
     return rope_qk_cfg(rot_dim, theta, layout, dict(scaling))
@@ -722,16 +731,15 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
     device = q.device
     given = out or ()
     _same(device, q, k, positions, *given)
-    ctx = _on(device, stream, q, k, positions, *given)
-    if ctx is not None:
-        with ctx:
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream, q, k, positions, *given):
             return rope_qk_t(q, k, positions, rot_dim, theta, layout, scaling, out)
     code = _dtype_code(q.dtype, fp32=True)
     N, Hq, D = q.shape
     ldq = _heads(q, "q")
     _int32(positions, "positions", (N,))
-    cfg = _rope_qk_cfg(D if rot_dim is None else rot_dim, theta, layout,
-                       tuple(scaling.items()) if scaling else ())
+    cfg = _rope_qk_cfg(D if rot_dim is None else int(rot_dim), float(theta), layout,
+                       _by_value(scaling) if scaling else ())
     Hk, ldk, kp = 0, 0, 0
     if k is not None:
         if k.dtype != q.dtype or k.dim() != 3 or k.shape[0] != N or k.shape[2] != D:
@@ -772,9 +780,8 @@ def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=N
     torch = _torch or _load_torch()
     device = x.device
     _same(device, x, w, bias, residual, out, workspace)
-    ctx = _on(device, stream, x, w, bias, residual, out, workspace)
-    if ctx is not None:
-        with ctx:
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream, x, w, bias, residual, out, workspace):
             return linear_t(x, w, bias, act, gated, residual, out, workspace)
     code = _dtype_code(x.dtype)
     if act not in ACTIVATIONS:
@@ -836,9 +843,8 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
     torch = _torch or _load_torch()
     device = q.device
     _same(device, q, k, v, cu_q, cu_k, key_mask, out, workspace)
-    ctx = _on(device, stream, q, k, v, cu_q, cu_k, key_mask, out, workspace)
-    if ctx is not None:
-        with ctx:
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream, q, k, v, cu_q, cu_k, key_mask, out, workspace):
             return cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q, max_k, key_mask, softmax_scale,
                                     out, return_lse, workspace)
     code = _dtype_code(q.dtype)

@@ -8,8 +8,8 @@ import math
 import numpy as np
 import pytest
 
-from test_layers_gpu import (_check_cross, _check_linear, _cross_case, _cu, _dtype, _f64, _h3,
-                             _linear_case, _run_cross, _u, _within)
+from test_layers_gpu import (_check_cross, _check_linear, _cross_case, _cu, _draw, _dtype, _f64,
+                             _h3, _linear_case, _run_cross, _u, _within)
 
 pytestmark = pytest.mark.gpu
 
@@ -254,6 +254,23 @@ def test_rope_angles_at_every_position(layout, scaling):
     bound = 2 * math.pi * (2.0 ** -26 + 2.0 ** -32 + 2.0 ** -34) + 2.0 ** -23 + 1e-15
     _within(_f64(y)[:, 0, first], np.cos(2 * math.pi * turns), bound, "cos")
     _within(_f64(y)[:, 0, second], np.sin(2 * math.pi * turns), bound, "sin")
+
+
+def test_rope_configuration_by_value():
+    """A configuration is what its numbers are at the call: objects that hold them may
+    change between calls."""
+    import torch
+    h3 = _h3()
+    q = _draw(np.random.default_rng(4), (40, 2, 64), torch.float32)
+    pos = torch.arange(40, dtype=torch.int32, device="cuda")
+    factor, theta = torch.tensor(2.0), torch.tensor(1e4)
+
+    def run(f, t):
+        return h3.rope_qk_t(q, None, pos, 64, t, "half", dict(kind="linear", factor=f))[0]
+
+    for f, t in ((2.0, 1e4), (5.0, 1e4), (5.0, 500.0)):
+        factor.fill_(f), theta.fill_(t)
+        assert torch.equal(run(factor, theta), run(f, t)), (f, t)
 
 
 # ------------------------------------------------------- streams, autograd, memory
