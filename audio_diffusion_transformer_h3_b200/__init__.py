@@ -619,13 +619,17 @@ def _on(device, stream, *tensors):
     """Context in which a call on ``stream`` (None: the device's current one)
     allocates and launches: that device is current, and what the call allocates
     belongs to that stream. The memory of ``tensors`` is not given out again
-    before a given stream has done what is on it by the time they are dropped."""
+    before a given stream has done what is on it by the time they are dropped,
+    unless it is the caller's (a raw handle, an ExternalStream): that one may end
+    before they do, and its caller keeps them."""
     torch = _torch or _load_torch()
     if stream is None:
         return torch.cuda.device(device)
     if isinstance(stream, int):   # (ExternalStream takes 0 for "a new one")
         stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                   else torch.cuda.default_stream(device))
+    if isinstance(stream, torch.cuda.ExternalStream):
+        tensors = ()
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, not on {device}")
     for t in tensors:

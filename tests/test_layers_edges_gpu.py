@@ -332,7 +332,7 @@ def test_inputs_of_a_call_on_another_stream_are_kept_until_it_is_done():
 
     def cross(x, w, pos, cu):
         return h3.cross_attn_fwd_t(x.view(rows, 32, 64), w.view(n, 32, 64), w.view(n, 32, 64), cu, cu,
-                                   rows, rows, stream=side.cuda_stream)
+                                   rows, rows, stream=side)
 
     for call in (linear, rope, cross):
         call(*inputs())
@@ -350,6 +350,28 @@ def test_inputs_of_a_call_on_another_stream_are_kept_until_it_is_done():
         assert busy and not old & {t.data_ptr() for t in new}, call.__name__
         del new, kept
         torch.cuda.synchronize()
+
+
+def test_a_raw_stream_may_end_before_its_tensors():
+    """A stream that is given by its handle belongs to the caller, who may destroy it
+    once it is done; tensors of calls on it are freed later."""
+    import ctypes
+
+    import torch
+    cudart = torch.cuda.cudart()
+    h3 = _h3()
+    handle = ctypes.c_void_p()
+    cudart.cudaStreamCreate(ctypes.addressof(handle))
+    x = torch.ones(256, 512, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(512, 512, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    y = h3.linear_t(x, w, stream=handle.value)
+    z = h3.linear_t(x, w, stream=torch.cuda.ExternalStream(handle.value))
+    torch.cuda.synchronize()
+    assert torch.equal(y, z) and (y == 512).all()
+    cudart.cudaStreamDestroy(handle.value)
+    del x, w
+    torch.cuda.synchronize()
 
 
 def test_tangents_are_refused():
