@@ -730,7 +730,8 @@ def rope_qk_t(q, k, positions, rot_dim: Optional[int] = None, theta: float = 100
     [N, Hq, D], k [N, Hk, D] or None, bf16, fp16 or fp32, heads contiguous (a
     token stride is free); positions int32 [N]. ``out``: (q_out, k_out), which
     may be (q, k). The gradient of q and k is this call on the outputs'
-    gradients with negated positions."""
+    gradients with negated positions. The tensors of a call on a raw handle or an
+    ExternalStream are the caller's to keep until that stream has done it."""
     torch = _torch or _load_torch()
     device = q.device
     given = out or ()
@@ -779,8 +780,13 @@ def linear_workspace_for(M: int, N: int, K: int, gated: bool = False, device=Non
 def linear_t(x, w, bias=None, act: str = "none", gated: bool = False, residual=None, out=None,
              workspace=None, stream=None):
     """act(x w^T + bias) + residual through h3_linear_fwd. x [M, K], w [N, K],
-    bf16 or fp16, rows 16-byte aligned (row strides a multiple of 8). ``gated``:
-    w [2N, K], act(first half) * (second half). ``out`` may be ``residual``."""
+    bf16 or fp16, rows 16-byte aligned (row strides a multiple of 8: where K is
+    not, x and w are views of wider rows; what lies behind K is not read).
+    ``gated``: w [2N, K], act(first half) * (second half). ``out`` may be
+    ``residual``. Without a ``workspace`` the call makes its own, and what it
+    reports there (device_status_t) cannot be asked for. The tensors of a call on
+    a raw handle or an ExternalStream are the caller's to keep until that stream
+    has done it."""
     torch = _torch or _load_torch()
     device = x.device
     _same(device, x, w, bias, residual, out, workspace)
@@ -843,7 +849,10 @@ def cross_attn_fwd_t(q, k, v, cu_q, cu_k, max_q: int, max_k: int, key_mask=None,
     k, v [Nk, Hk, D], bf16 or fp16, heads contiguous, token strides a multiple
     of 8; cu_q, cu_k int32 [nseg + 1]; key_mask bool or uint8 [Nk], False: no
     query attends to this key. A row without keys gets 0 (LSE -inf). Rows
-    behind cu_q[-1] are not written."""
+    behind cu_q[-1] are not written, and none is where the lengths are not as
+    said: a caller who cannot vouch for them passes a ``workspace`` and asks
+    device_status_t for it. The tensors of a call on a raw handle or an
+    ExternalStream are the caller's to keep until that stream has done it."""
     torch = _torch or _load_torch()
     device = q.device
     _same(device, q, k, v, cu_q, cu_k, key_mask, out, workspace)

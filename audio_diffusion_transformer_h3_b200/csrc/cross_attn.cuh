@@ -29,8 +29,9 @@
 // chunks so that all SMs read. Each tile then leaves its unnormalised O, m and
 // l in fp32, and cross_join_kernel adds a row's parts up in their order.
 //
-// Measured: 8320 rows x 56 heads of 128 on 2048 keys 421 us (1160 TFLOP/s, the
-// dense self attention's rate), on 512 keys 125 us: a key tile costs 1.9 us for
+// Measured, in a loop that leaves K, V and the output's memory in L2: 8320 rows x 56
+// heads of 128 on 2048 keys 421 us (1160 TFLOP/s, the dense self attention's rate), on
+// 512 keys 127 us (145 to 151 where the output's lines are not in L2): a key tile costs 1.9 us for
 // both query tiles, bound by the softmax, an item another 2 us, in which the
 // tensor cores wait for the last P, the output and the next first scores. 64 rows
 // on 33280 keys of 24 heads of 64: 63 us (3.2 TB/s), with a mask 74.
@@ -63,7 +64,9 @@ struct CrossParams {
 };
 
 constexpr int kCrossTable = 256;        // entries of the segment table
-constexpr int kCrossItems = 296;        // items that a split aims at: two for each of 148 SMs
+// items that a split aims at: two for each of B200's 148 SMs (a constant: the workspace's
+// size hangs on it, which is asked for without a device)
+constexpr int kCrossItems = 296;
 constexpr int kCrossMinChunk = 2;       // key tiles of a chunk at least
 
 // An item in the ring (byte offsets).
@@ -727,7 +730,10 @@ __global__ void __launch_bounds__(384, 1)
                 const float nm = P_SHIFT - (m == -INFINITY ? 0.0f : m);
                 uint64_t acc0 = 0, acc1 = 0;
                 const uint64_t s2 = f2_splat(sl2), n2 = f2_splat(nm);
-                // P of keys [32 h, 32 h + 32). All exponentials on MUFU: with three pairs of
+                // P of keys [32 h, 32 h + 32): to T for the PV product (kind::f16 takes A
+                // and B of one 16-bit type), into the sum as it is. That rounding adds about
+                // as much error as O's own (bf16, against 64 bits: 1.7e-3 with P in fp32,
+                // 2.3e-3 so). All exponentials on MUFU: with three pairs of
                 // eight as polynomials on the FMA pipe, as the dense kernel has them, the
                 // packed clips took 2 % longer
                 auto exp_part = [&](const int h) {

@@ -5,9 +5,9 @@
 // by tcgen05.mma into fp32 TMEM accumulators, every wait bounded:
 //   linear_tile_kernel  rows of x are the 128 rows of the MMA, 32 to 256 weight rows
 //       its columns. Persistent, two accumulators, so that a tile's epilogue
-//       runs under the next tile's main loop. Bound by the tensor cores: 71 % of
-//       their cycles in a single launch of 4160 x 7168 x 5376 (239 us), 1170 to
-//       1300 TFLOP/s in a loop under the power cap (8320 rows).
+//       runs under the next tile's main loop. Bound by the tensor cores: 73 % of
+//       their cycles in a single launch of 4160 x 7168 x 5376 (232 us), 1155 to
+//       1350 TFLOP/s in a loop under the power cap (8320 rows).
 //   linear_skinny_kernel  few rows of x: weight rows are the MMA's 128 rows
 //       and x its 16..128 columns, so nothing of the MMA is spent on absent
 //       rows. Bound by reading w once; to have all SMs read, the sum over K

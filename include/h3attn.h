@@ -386,7 +386,8 @@ size_t h3_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act);
  *   dtype H3_BF16 or H3_FP16.
  *   workspace: device, 256-byte aligned, >= h3_linear_workspace_size bytes;
  *              not shared by calls that run concurrently.
- * fp32 accumulation, bias, activation and residual in fp32, one rounding.
+ * fp32 accumulation, bias, activation and residual in fp32 (exponentials,
+ * quotients and the erf to a few 2^-22 of themselves), one rounding.
  * Deterministic (also where the sum over K is split: the parts are added in
  * their order). One kernel launch. What the device finds (a bounded wait that
  * gave up) stands in the workspace's status word (h3_read_device_status), which
@@ -429,8 +430,9 @@ size_t h3_cross_workspace_size(int64_t Nq, int32_t Hq, int32_t Hk, int32_t D, in
  *              softmax_scale finite (times log2 e too), >= 0; dtype H3_BF16 or H3_FP16.
  *   workspace: device, 256-byte aligned, >= h3_cross_workspace_size bytes; not
  *              shared by calls that run concurrently.
- * fp32 scores, sums and accumulation; P is rounded to dtype before the PV
- * product. Deterministic, the split over keys included. Launches: the attention
+ * fp32 scores, sums and accumulation; exponentials to 2^-22 of themselves; P is
+ * rounded to dtype before the PV product (the tensor cores take no wider type
+ * beside v), the row's sum and LSE take it unrounded. Deterministic, the split over keys included. Launches: the attention
  * kernel and, where it splits the keys, one that joins the parts. The status word
  * is reset by every call. */
 h3_status h3_cross_attn_fwd(const void *q, int64_t ldq, const void *k, int64_t ldk,
