@@ -6,7 +6,7 @@
 //   linear_tile_kernel  rows of x are the 128 rows of the MMA, 32 to 256 weight rows
 //       its columns. Persistent, two accumulators, so that a tile's epilogue
 //       runs under the next tile's main loop. Bound by the tensor cores: 73 % of
-//       their cycles in a single launch of 4160 x 7168 x 5376 (232 us), 1155 to
+//       their cycles in a single launch of 4160 x 7168 x 5376 (232 us), 1140 to
 //       1350 TFLOP/s in a loop under the power cap (8320 rows).
 //   linear_skinny_kernel  few rows of x: weight rows are the MMA's 128 rows
 //       and x its 16..128 columns, so nothing of the MMA is spent on absent
